@@ -263,6 +263,141 @@ int moe_expert_balance(const moe_shape_t* shape, const void* u, const void* E,
                        const float* bias, const int32_t* counts, float* f,
                        float* P, void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Training operators: what a training step of the experts is made of.
+ *
+ *   x = moe_layer_norm(u)                        the norm in front of the layer
+ *   moe_route, moe_dispatch, rows gathered by perm
+ *   gu = moe_grouped_matmul(x_rows, W13)         packed gate/up columns
+ *   a  = moe_swiglu(gu)
+ *   y  = moe_grouped_matmul(a, W2)               -> moe_combine
+ *   da = moe_grouped_matmul_dx(dy, W2)           dW2  = moe_grouped_matmul_dw(dy, a)
+ *   dgu = moe_swiglu_backward(gu, da)
+ *   dx = moe_grouped_matmul_dx(dgu, W13)         dW13 = moe_grouped_matmul_dw(dgu, x_rows)
+ *   du = moe_layer_norm_backward(...)
+ *   update = moe_orthogonalize(momentum of dW)
+ *
+ * The conventions at the top of this file hold: device pointers, dense
+ * row-major tensors, 16-byte aligned, asynchronous on `stream`, no
+ * allocation, bitwise reproducible, capturable.  An output overlaps no input
+ * unless its function says so.  A call that takes `ws` writes there: calls
+ * that may run at the same time, replays of captured ones among them, need a
+ * workspace each.
+ * ------------------------------------------------------------------------- */
+
+/* Ragged groups of rows, each with its own matrix: group g owns the rows
+   offsets[g] .. offsets[g+1]-1 (device int32 [n_groups + 1], as moe_dispatch
+   writes them) and W_g, row-major [n, k] in W [n_groups, n, k].  Groups may be
+   empty.  Offsets are expected non-decreasing in [0, rows]; a start is clamped
+   to that range and an end to [its start, rows], so that no offsets reach
+   outside the tensors.  Rows that no group owns are not read and not
+   written.
+   Limits: 1 <= n_groups <= 256, 0 <= rows <= 2^31 - 512, 1 <= n, k <= 2^24;
+   bf16: n and k multiples of 8; fp32 runs on the CUDA cores.  The products'
+   64 x 64 output tiles must number fewer than 2^31, and the tensors be smaller
+   than 2^40 bytes. */
+typedef struct {
+  int64_t rows;     /* rows of X, Y, dY and dX */
+  int32_t n_groups;
+  int32_t n;        /* columns of Y and dY, rows of one W */
+  int32_t k;        /* columns of X and dX, columns of one W */
+  int32_t dtype;    /* MOE_DTYPE_* of X, Y, dY, dX and W */
+  int32_t flags;    /* MOE_GROUPED_* */
+} moe_grouped_shape_t;
+
+enum {
+  /* dW is float32 instead of `dtype`. */
+  MOE_GROUPED_DW_F32 = 1,
+  /* dW += the gradient; dW must be float32 (dtype F32 or the flag above). */
+  MOE_GROUPED_DW_ACCUMULATE = 2,
+};
+
+int moe_grouped_workspace_size(const moe_grouped_shape_t* shape, size_t* bytes);
+
+/* Y[r] = W_g X[r] for every row r of group g.  X [rows, k], Y [rows, n]. */
+int moe_grouped_matmul(const moe_grouped_shape_t* shape, const void* X, const int32_t* offsets,
+                       const void* W, void* Y, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Input gradient: dX[r] = W_g^T dY[r].  dY [rows, n], dX [rows, k]. */
+int moe_grouped_matmul_dx(const moe_grouped_shape_t* shape, const void* dY, const int32_t* offsets,
+                          const void* W, void* dX, void* ws, size_t ws_bytes,
+                          moe_stream_t stream);
+
+/* Weight gradient: dW_g = sum over the group's rows of dY[r] X[r]^T, zero for
+   an empty group (left as it is with MOE_GROUPED_DW_ACCUMULATE).
+   dW [n_groups, n, k], every element written.  fp32 accumulation; for bf16
+   inputs it is the tensor cores' own, which truncates: a float32 dW is off by
+   about 1e-9 times the group's rows, relative to its norm. */
+int moe_grouped_matmul_dw(const moe_grouped_shape_t* shape, const void* dY, const void* X,
+                          const int32_t* offsets, void* dW, void* ws, size_t ws_bytes,
+                          moe_stream_t stream);
+
+/* SwiGLU on packed gate/up columns: a row of gu [rows, 2*inter] holds, for
+   each block of 64 intermediate columns, 64 gate values g and then the 64 up
+   values u (the product of a row with moe_pack_w13's W13).
+   0 <= rows < 2^31, inter a positive multiple of 64, at most 2^24. */
+typedef struct {
+  int64_t rows;
+  int32_t inter;
+  int32_t dtype;
+} moe_swiglu_shape_t;
+
+/* a = SiLU(g) * u.  a [rows, inter]. */
+int moe_swiglu(const moe_swiglu_shape_t* shape, const void* gu, void* a, moe_stream_t stream);
+
+/* With s = 1 / (1 + e^-g): dg = da * u * s * (1 + g (1 - s)), du = da * g * s,
+   packed like gu into dgu [rows, 2*inter], which may be gu itself. */
+int moe_swiglu_backward(const moe_swiglu_shape_t* shape, const void* gu, const void* da, void* dgu,
+                        moe_stream_t stream);
+
+/* Layer norm of each row of x [T, d]: y = (x - mean) * rstd * gamma + beta,
+   rstd = 1 / sqrt(var + eps), var = mean (x - mean)^2, all in fp32.
+   0 <= T < 2^31, 1 <= d <= 2^24, eps finite and >= 0. */
+typedef struct {
+  int64_t T;
+  int32_t d;
+  int32_t dtype;  /* of x, y, dy and dx */
+  float eps;
+} moe_norm_shape_t;
+
+/* gamma [d] and beta [d] (NULL: none) are float32.  mean and rstd [T] float32
+   are kept for the backward pass; either may be NULL.  y may be x. */
+int moe_layer_norm(const moe_norm_shape_t* shape, const void* x, const float* gamma,
+                   const float* beta, void* y, float* mean, float* rstd, moe_stream_t stream);
+
+int moe_layer_norm_workspace_size(const moe_norm_shape_t* shape, size_t* bytes);
+
+/* The gradients of moe_layer_norm from its input x and its mean and rstd:
+   dx [T, d], dgamma [d] and dbeta [d] (NULL: not wanted) float32.  dx may be
+   dy.  For T = 0 dgamma and dbeta are zero. */
+int moe_layer_norm_backward(const moe_norm_shape_t* shape, const void* dy, const void* x,
+                            const float* gamma, const float* mean, const float* rstd, void* dx,
+                            float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
+
+/* Newton-Schulz orthogonalisation of n_mats matrices M [n_mats, rows, cols]
+   (the Muon optimiser's update): X = M / (|M|_F + 1e-7), then `steps` times
+   A = X X^T (for rows > cols the transpose's), X <- a X + (b A + c A A) X.
+   `coef` is HOST memory, (a, b, c) for each step, read before the call
+   returns; NULL means 3.4445, -4.7750, 2.0315 in each.  O [n_mats, rows,
+   cols] is bfloat16, whatever the dtype of M.  The products run on the tensor
+   cores with fp16 operands beside a 22-bit X, which needs the coefficients to
+   keep the singular values of every step's X below about 100.  A matrix of
+   zeros gives zeros; one with an infinity or NaN gives NaN, the others of the
+   stack are untouched by it.  M's tensor may have any 1 <= rows, cols <=
+   65536; n_mats <= 65535; 1 <= steps <= 16. */
+typedef struct {
+  int32_t n_mats;
+  int32_t rows;
+  int32_t cols;
+  int32_t steps;
+  int32_t dtype;  /* of M */
+} moe_ortho_shape_t;
+
+int moe_orthogonalize_workspace_size(const moe_ortho_shape_t* shape, size_t* bytes);
+int moe_orthogonalize(const moe_ortho_shape_t* shape, const float* coef, const void* M, void* O,
+                      void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Copies the workspace status word (0 or MOE_ERR_DEVICE_CHECK) to *status
    and clears it; synchronises `stream`. */
 int moe_read_status(const void* ws, int32_t* status, moe_stream_t stream);
@@ -290,6 +425,14 @@ enum {
   MOE_KERNEL_PACK = 9,
   MOE_KERNEL_BALANCE = 10,
   MOE_KERNEL_DECODE_LAYER = 11, /* the whole layer for decode-sized batches */
+  MOE_KERNEL_GROUPED_FWD = 12,
+  MOE_KERNEL_GROUPED_DX = 13,
+  MOE_KERNEL_GROUPED_DW = 14,
+  MOE_KERNEL_SWIGLU = 15,
+  MOE_KERNEL_SWIGLU_BACKWARD = 16,
+  MOE_KERNEL_LAYER_NORM = 17,
+  MOE_KERNEL_LAYER_NORM_BACKWARD = 18,
+  MOE_KERNEL_ORTHOGONALIZE = 19,
 };
 int moe_profile_enable(int on);
 int moe_profile_read(int32_t* kinds, float* ms, int32_t max, int32_t* count);

@@ -46,6 +46,16 @@ MOE_KERNEL_MEMSET = 8
 MOE_KERNEL_PACK = 9
 MOE_KERNEL_BALANCE = 10
 MOE_KERNEL_DECODE_LAYER = 11
+MOE_KERNEL_GROUPED_FWD = 12
+MOE_KERNEL_GROUPED_DX = 13
+MOE_KERNEL_GROUPED_DW = 14
+MOE_KERNEL_SWIGLU = 15
+MOE_KERNEL_SWIGLU_BACKWARD = 16
+MOE_KERNEL_LAYER_NORM = 17
+MOE_KERNEL_LAYER_NORM_BACKWARD = 18
+MOE_KERNEL_ORTHOGONALIZE = 19
+MOE_GROUPED_DW_F32 = 1
+MOE_GROUPED_DW_ACCUMULATE = 2
 MOE_PATH_STAGES = 0
 MOE_PATH_DECODE_LAYER = 1
 MOE_PATH_SMALL_BATCH = 2
@@ -68,7 +78,29 @@ class MoeShape(ctypes.Structure):
                 f"dtype={self.dtype}, flags={self.flags})")
 
 
+class MoeGroupedShape(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("n_groups", c_int32), ("n", c_int32), ("k", c_int32),
+                ("dtype", c_int32), ("flags", c_int32)]
+
+
+class MoeSwigluShape(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("inter", c_int32), ("dtype", c_int32)]
+
+
+class MoeNormShape(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("d", c_int32), ("dtype", c_int32), ("eps", ctypes.c_float)]
+
+
+class MoeOrthoShape(ctypes.Structure):
+    _fields_ = [("n_mats", c_int32), ("rows", c_int32), ("cols", c_int32), ("steps", c_int32),
+                ("dtype", c_int32)]
+
+
 _SHAPE = POINTER(MoeShape)
+_GROUPED = POINTER(MoeGroupedShape)
+_SWIGLU = POINTER(MoeSwigluShape)
+_NORM = POINTER(MoeNormShape)
+_ORTHO = POINTER(MoeOrthoShape)
 _V = c_void_p
 
 # name -> (restype, argtypes)
@@ -88,6 +120,17 @@ SIGNATURES = {
     "moe_layer_forward": (c_int, [_SHAPE, _V, _V, _V, _V, _V, _V, _V, _V, _V, c_size_t, _V]),
     "moe_layer_forward_host": (c_int, [_SHAPE, _V, _V, _V, _V, _V, _V, _V, _V, _V, c_size_t, _V]),
     "moe_expert_balance": (c_int, [_SHAPE, _V, _V, _V, _V, _V, _V, _V, c_size_t, _V]),
+    "moe_grouped_workspace_size": (c_int, [_GROUPED, POINTER(c_size_t)]),
+    "moe_grouped_matmul": (c_int, [_GROUPED, _V, _V, _V, _V, _V, c_size_t, _V]),
+    "moe_grouped_matmul_dx": (c_int, [_GROUPED, _V, _V, _V, _V, _V, c_size_t, _V]),
+    "moe_grouped_matmul_dw": (c_int, [_GROUPED, _V, _V, _V, _V, _V, c_size_t, _V]),
+    "moe_swiglu": (c_int, [_SWIGLU, _V, _V, _V]),
+    "moe_swiglu_backward": (c_int, [_SWIGLU, _V, _V, _V, _V]),
+    "moe_layer_norm": (c_int, [_NORM, _V, _V, _V, _V, _V, _V, _V]),
+    "moe_layer_norm_workspace_size": (c_int, [_NORM, POINTER(c_size_t)]),
+    "moe_layer_norm_backward": (c_int, [_NORM, _V, _V, _V, _V, _V, _V, _V, _V, _V, c_size_t, _V]),
+    "moe_orthogonalize_workspace_size": (c_int, [_ORTHO, POINTER(c_size_t)]),
+    "moe_orthogonalize": (c_int, [_ORTHO, POINTER(ctypes.c_float), _V, _V, _V, c_size_t, _V]),
     "moe_read_status": (c_int, [_V, POINTER(c_int32), _V]),
     "moe_profile_enable": (c_int, [c_int]),
     "moe_profile_read": (c_int, [POINTER(c_int32), POINTER(ctypes.c_float), c_int32,
@@ -231,6 +274,99 @@ def moe_expert_balance(shape, u, E, bias, counts, f, P, ws, ws_bytes=None, strea
     return _check("moe_expert_balance", lib().moe_expert_balance(
         ctypes.byref(shape), _ptr(u), _ptr(E), _ptr(bias), _ptr(counts), _ptr(f), _ptr(P),
         _ptr(ws), nb, _stream(stream)))
+
+
+# ------------------------------------------------------- training operators
+def make_grouped_shape(rows, n_groups, n, k, dtype=MOE_DTYPE_BF16, flags=0) -> MoeGroupedShape:
+    return MoeGroupedShape(rows, n_groups, n, k, dtype, flags)
+
+
+def make_swiglu_shape(rows, inter, dtype=MOE_DTYPE_BF16) -> MoeSwigluShape:
+    return MoeSwigluShape(rows, inter, dtype)
+
+
+def make_norm_shape(T, d, dtype=MOE_DTYPE_BF16, eps=1e-5) -> MoeNormShape:
+    return MoeNormShape(T, d, dtype, eps)
+
+
+def make_ortho_shape(n_mats, rows, cols, steps=5, dtype=MOE_DTYPE_BF16) -> MoeOrthoShape:
+    return MoeOrthoShape(n_mats, rows, cols, steps, dtype)
+
+
+def _size(fn, shape) -> int:
+    n = c_size_t(0)
+    _check(fn, getattr(lib(), fn)(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def moe_grouped_workspace_size(shape: MoeGroupedShape) -> int:
+    return _size("moe_grouped_workspace_size", shape)
+
+
+def moe_layer_norm_workspace_size(shape: MoeNormShape) -> int:
+    return _size("moe_layer_norm_workspace_size", shape)
+
+
+def moe_orthogonalize_workspace_size(shape: MoeOrthoShape) -> int:
+    return _size("moe_orthogonalize_workspace_size", shape)
+
+
+def _ws_bytes(ws, ws_bytes):
+    return ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+
+
+def moe_grouped_matmul(shape, X, offsets, W, Y, ws, ws_bytes=None, stream=None):
+    return _check("moe_grouped_matmul", lib().moe_grouped_matmul(
+        ctypes.byref(shape), _ptr(X), _ptr(offsets), _ptr(W), _ptr(Y), _ptr(ws),
+        _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_grouped_matmul_dx(shape, dY, offsets, W, dX, ws, ws_bytes=None, stream=None):
+    return _check("moe_grouped_matmul_dx", lib().moe_grouped_matmul_dx(
+        ctypes.byref(shape), _ptr(dY), _ptr(offsets), _ptr(W), _ptr(dX), _ptr(ws),
+        _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_grouped_matmul_dw(shape, dY, X, offsets, dW, ws, ws_bytes=None, stream=None):
+    return _check("moe_grouped_matmul_dw", lib().moe_grouped_matmul_dw(
+        ctypes.byref(shape), _ptr(dY), _ptr(X), _ptr(offsets), _ptr(dW), _ptr(ws),
+        _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_swiglu(shape, gu, a, stream=None):
+    return _check("moe_swiglu", lib().moe_swiglu(ctypes.byref(shape), _ptr(gu), _ptr(a),
+                                                 _stream(stream)))
+
+
+def moe_swiglu_backward(shape, gu, da, dgu, stream=None):
+    return _check("moe_swiglu_backward", lib().moe_swiglu_backward(
+        ctypes.byref(shape), _ptr(gu), _ptr(da), _ptr(dgu), _stream(stream)))
+
+
+def moe_layer_norm(shape, x, gamma, beta, y, mean, rstd, stream=None):
+    return _check("moe_layer_norm", lib().moe_layer_norm(
+        ctypes.byref(shape), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd),
+        _stream(stream)))
+
+
+def moe_layer_norm_backward(shape, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, ws_bytes=None,
+                            stream=None):
+    return _check("moe_layer_norm_backward", lib().moe_layer_norm_backward(
+        ctypes.byref(shape), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx),
+        _ptr(dgamma), _ptr(dbeta), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_orthogonalize(shape, M, O, ws, ws_bytes=None, coef=None, stream=None):
+    """`coef`: 3 * shape.steps host floats (a, b, c per step), or None for
+    the library's own."""
+    if coef is not None:
+        coef = [float(c) for c in coef]
+        if len(coef) != 3 * shape.steps:
+            raise ValueError(f"coef holds {len(coef)} numbers, not 3 * {shape.steps}")
+        coef = (ctypes.c_float * len(coef))(*coef)
+    return _check("moe_orthogonalize", lib().moe_orthogonalize(
+        ctypes.byref(shape), coef, _ptr(M), _ptr(O), _ptr(ws), _ws_bytes(ws, ws_bytes),
+        _stream(stream)))
 
 
 def moe_read_status(ws, stream=None) -> int:

@@ -10,6 +10,7 @@
 #include "decode_fused.h"
 #include "gemm_sm100.h"
 #include "kernels.h"
+#include "train_kernels.h"
 
 namespace moe {
 
@@ -462,6 +463,14 @@ int host_pipe(int nc, HostPipe** out) {
 }
 
 }  // namespace
+
+int require_device(int* sms) {
+  DeviceInfo di;
+  if (int rc = device_info(&di)) return rc;
+  *sms = di.sms;
+  return MOE_OK;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -533,6 +542,14 @@ const char* moe_kernel_name(int32_t kind) {
     case MOE_KERNEL_PACK: return "pack_w13";
     case MOE_KERNEL_BALANCE: return "expert_balance";
     case MOE_KERNEL_DECODE_LAYER: return "decode_layer";
+    case MOE_KERNEL_GROUPED_FWD: return "grouped_matmul";
+    case MOE_KERNEL_GROUPED_DX: return "grouped_matmul_dx";
+    case MOE_KERNEL_GROUPED_DW: return "grouped_matmul_dw";
+    case MOE_KERNEL_SWIGLU: return "swiglu";
+    case MOE_KERNEL_SWIGLU_BACKWARD: return "swiglu_backward";
+    case MOE_KERNEL_LAYER_NORM: return "layer_norm";
+    case MOE_KERNEL_LAYER_NORM_BACKWARD: return "layer_norm_backward";
+    case MOE_KERNEL_ORTHOGONALIZE: return "orthogonalize";
     default: return "unknown";
   }
 }

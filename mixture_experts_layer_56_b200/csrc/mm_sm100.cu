@@ -1,0 +1,679 @@
+// Matrix products of the training operators on CTA pairs (tcgen05
+// cta_group::2): D[m, n] = sum_k A(m, k) B(n, k), fp32 accumulation in TMEM.
+//
+//   forward          Y[r]  = X[r] W_g^T      NT, ragged rows
+//   input gradient   dX[r] = dY[r] W_g       NN, ragged rows
+//   weight gradient  dW_g  = dY_g^T X_g      TN, ragged reduction
+//   Newton-Schulz    X X^T, A A, B X         any, a batch of equal matrices
+//
+// No operand is transposed in memory.  A TMA box is 64 elements (128 bytes,
+// swizzled) of the memory rows; where those run along m or n instead of k the
+// box holds 64 k rows of one 64-wide slice, and the MMA's descriptor and the
+// instruction's major bit say so.
+//
+// A tile is 256 x 256, its rows split over the two SMs of a cluster: each CTA
+// loads its 128 rows of A and its half of B's 256 rows, and the leader issues
+// M = 256, N = 256 MMAs for both.  Six 32 KB stages per CTA; the accumulator
+// is double-buffered in TMEM (2 x 256 columns), so that the epilogue of one
+// tile runs under the MMAs of the next.  Warps: 0 TMA, 1 MMA, 2 TMEM, 3 the
+// ragged reduction's zeroing, 4-11 epilogue.
+//
+// Ragged rows need no masking: a tile may run past its group's last row, and
+// the rows it computes there are not stored.  A ragged reduction does: the
+// last k-block of a group holds the first rows of the next one (or rows that
+// nobody owns, which may hold NaN).  Warp 3 of each CTA zeroes those rows of
+// both operands in shared memory before the MMAs may read them.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "mm_sm100.h"
+#include "mm_ptx.cuh"
+
+namespace moe {
+namespace sm100 {
+
+namespace {
+
+constexpr int kTile = 256;      // rows and columns of a pair's tile
+constexpr int kHalf = 128;      // rows of A, and of B, per CTA
+constexpr int kKB = 64;         // k-block
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kStagePitch = 128 + 16;  // staging row: 128 bytes, padded off the bank period
+constexpr int kWarpStage = 32 * kStagePitch;
+constexpr uint32_t kOpBytes = kHalf * kKB * 2;       // one operand of a stage
+constexpr uint32_t kStageBytes = 2 * kOpBytes;
+constexpr uint32_t kChunkBytes = 64 * kKB * 2;       // an MN-major 64-wide slice
+constexpr int kStages = 5;
+constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kWarpStage + 1024;
+constexpr int kColChunk = 8;  // N tiles that a group's row blocks sweep together
+
+// Rows of 32 lanes (lane r holds row r, NV 16-byte pieces) written to global
+// memory as whole row segments through the warp's staging area.  `dst` is the
+// lane's row start (nullptr: not written) and `pieces` how many of the NV
+// pieces lie inside the matrix.
+template <int NV, typename Put>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint4* v, uint8_t* dst, int pieces,
+                                           int lane, Put put) {
+  constexpr int RPI = 32 / NV;
+#pragma unroll
+  for (int c = 0; c < NV; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * kStagePitch + c * 16) = v[c];
+  __syncwarp();
+#pragma unroll
+  for (int it = 0; it < NV; ++it) {
+    const int row = it * RPI + lane / NV;
+    const int c = lane % NV;
+    uint8_t* rdst = reinterpret_cast<uint8_t*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + row * kStagePitch + c * 16);
+    if (rdst != nullptr && c < pieces) put(reinterpret_cast<uint4*>(rdst + c * 16), x);
+  }
+  __syncwarp();
+}
+
+struct PutPlain {
+  __device__ __forceinline__ void operator()(uint4* p, uint4 x) const { *p = x; }
+};
+struct PutAddF32 {
+  __device__ __forceinline__ void operator()(uint4* p, uint4 x) const {
+    float4 o = *reinterpret_cast<float4*>(p);
+    o.x += __uint_as_float(x.x);
+    o.y += __uint_as_float(x.y);
+    o.z += __uint_as_float(x.z);
+    o.w += __uint_as_float(x.w);
+    *reinterpret_cast<float4*>(p) = o;
+  }
+};
+
+__device__ __forceinline__ uint4 pack_half8(const float* x) {
+  uint4 v;
+  __half2* h = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+  return v;
+}
+__device__ __forceinline__ void unpack_half8(const uint4& v, float* x) {
+  const __half2* h = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(h[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+struct Tile {
+  int g, m_blk, n_blk;
+  int row0;  // ragged: the group's first row
+  int rows;  // rows of D of the group (ragged rows, or m), or the ragged reduction's length
+  int nkb;   // k-blocks
+};
+
+template <int LAYOUT, int SCHED, int EPI, bool FP16>
+__global__ void __launch_bounds__(kThreads, 1)
+mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const MmArgs args) {
+  constexpr bool A_MN = LAYOUT == kMmTN;
+  constexpr bool B_MN = LAYOUT != kMmNT;
+  constexpr bool RAG_M = SCHED == kMmRaggedM;
+  constexpr bool RAG_K = SCHED == kMmRaggedK;
+  constexpr bool SYM = SCHED == kMmBatchSym;
+  constexpr uint32_t IDESC = idesc_16bit_f32(kTile, kTile, FP16, A_MN, B_MN);
+  constexpr uint32_t TMEM_COLS = 2 * kTile;
+  constexpr uint16_t kBoth = 0x3;
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[3 * kStages + 5];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ int32_t tile_start[kMmMaxGroups + 1];
+  __shared__ int32_t grp_row0[kMmMaxGroups];
+  __shared__ int32_t grp_rows[kMmMaxGroups];
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t smem_base = smem_addr(smem);
+  const uint32_t bar_base = smem_addr(bars);
+  auto full_bar = [&](int s) { return bar_base + 8u * s; };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (kStages + s); };
+  auto land_bar = [&](int s) { return bar_base + 8u * (2 * kStages + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (3 * kStages + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (3 * kStages + 2 + a); };
+  const uint32_t drain_bar = bar_base + 8u * (3 * kStages + 4);
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cluster = static_cast<int>(cluster_id_x());
+  const int nclusters = static_cast<int>(num_clusters_x());
+  const int G = args.groups;
+  const int nt = (args.n + kTile - 1) / kTile;
+  volatile int* abort_p = &abort_flag;
+
+  // ---- setup --------------------------------------------------------------
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      // the leader's arrive (+ both CTAs' bytes); with a ragged reduction
+      // either CTA arrives, its rows zeroed where the k-block is a group's last
+      mbar_init(full_bar(s), RAG_K ? 2 : 1);
+      mbar_init(empty_bar(s), 1);  // one multicast commit
+      mbar_init(land_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * kEpiWarps);  // epilogue warps of both CTAs (leader's copy)
+    }
+    mbar_init(drain_bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    fence_async_shared();
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(smem_addr(&tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (RAG_M || RAG_K) {
+    // Offsets are held to 0 <= first <= last <= rows, so that no value of
+    // them reaches outside the operands.
+    for (int g = tid; g < G; g += kThreads) {
+      const int a = min(max(args.offsets[g], 0), args.rows);
+      const int b = min(max(args.offsets[g + 1], a), args.rows);
+      grp_row0[g] = a;
+      grp_rows[g] = b - a;
+      tile_start[g + 1] = ((b - a + kTile - 1) / kTile) * nt;
+    }
+    __syncthreads();
+    if (RAG_M && warp == 0) {
+      const int per = (G + 31) / 32;
+      const int beg = min(lane * per, G);
+      const int end = min(beg + per, G);
+      int sum = 0;
+      for (int i = beg; i < end; ++i) sum += tile_start[i + 1];
+      int incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      int run = incl - sum;
+      for (int i = beg; i < end; ++i) {
+        run += tile_start[i + 1];
+        tile_start[i + 1] = run;
+      }
+      if (lane == 0) tile_start[0] = 0;
+    }
+  }
+  tc_fence_before();
+  cluster_sync_all();  // barrier inits and TMEM allocations visible to the pair
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  const int mt_fixed = RAG_M ? 0 : (args.m + kTile - 1) / kTile;
+  const int per_group = SYM ? mt_fixed * (mt_fixed + 1) / 2 : mt_fixed * nt;
+  const int total_tiles = RAG_M ? tile_start[G] : G * per_group;
+
+  auto tile_of = [&](int t) {
+    Tile ti;
+    if (RAG_M) {
+      int lo = 0, hi = G - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tile_start[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      // a group's row blocks sweep kColChunk column tiles together, so that
+      // the pairs in flight share a slice of the group's matrix in L2
+      ti.g = lo;
+      const int local = t - tile_start[lo];
+      const int mt = (tile_start[lo + 1] - tile_start[lo]) / nt;
+      const int cw = min(kColChunk, nt);
+      const int c = local / (cw * mt);
+      const int rem = local - c * cw * mt;
+      const int wc = min(cw, nt - c * cw);
+      ti.m_blk = rem / wc;
+      ti.n_blk = c * cw + (rem - ti.m_blk * wc);
+      ti.row0 = grp_row0[lo];
+      ti.rows = grp_rows[lo];
+      ti.nkb = (args.k + kKB - 1) / kKB;
+    } else {
+      ti.g = t / per_group;
+      const int local = t - ti.g * per_group;
+      if (SYM) {
+        int mb = static_cast<int>((sqrtf(8.0f * local + 1.0f) - 1.0f) * 0.5f);
+        while (mb * (mb + 1) / 2 > local) --mb;
+        while ((mb + 1) * (mb + 2) / 2 <= local) ++mb;
+        ti.m_blk = mb;
+        ti.n_blk = local - mb * (mb + 1) / 2;
+      } else {
+        ti.m_blk = local / nt;
+        ti.n_blk = local - ti.m_blk * nt;
+      }
+      ti.row0 = RAG_K ? grp_row0[ti.g] : 0;
+      ti.rows = RAG_K ? grp_rows[ti.g] : args.m;
+      ti.nkb = ((RAG_K ? ti.rows : args.k) + kKB - 1) / kKB;
+    }
+    return ti;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------- TMA producer ----
+    if (lane == 0) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_parity = 0;
+      bool ok = true;
+      for (int tile = cluster; tile < total_tiles && ok; tile += nclusters) {
+        const Tile ti = tile_of(tile);
+        const int m0 = ti.m_blk * kTile + static_cast<int>(rank) * kHalf;
+        const int n0 = ti.n_blk * kTile + static_cast<int>(rank) * kHalf;
+        const int za = RAG_M || RAG_K ? 0 : ti.g;
+        const int zb = RAG_K ? 0 : ti.g;
+        for (int kb = 0; kb < ti.nkb; ++kb) {
+          if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_p, args.status)) { ok = false; break; }
+          const uint32_t sa = smem_base + stage * kStageBytes;
+          const uint32_t sb = sa + kOpBytes;
+          // a ragged group's last, partial k-block lands on this CTA's own
+          // barrier, where warp 3 takes it over
+          const bool partial = RAG_K && kb == ti.nkb - 1 && (ti.rows & (kKB - 1)) != 0;
+          uint32_t fb;
+          if (partial) {
+            fb = land_bar(stage);
+            mbar_arrive_expect_tx(fb, kStageBytes);
+          } else {
+            fb = leader ? full_bar(stage) : map_to_cta(full_bar(stage), 0);
+            if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);
+            else if (RAG_K) mbar_arrive_cluster(fb);
+          }
+          const int k0 = kb * kKB + (RAG_K ? ti.row0 : 0);
+          if (A_MN) {
+            tma_load_3d_pair(sa, &tmA, fb, m0, k0, za);
+            tma_load_3d_pair(sa + kChunkBytes, &tmA, fb, m0 + 64, k0, za);
+          } else {
+            tma_load_3d_pair(sa, &tmA, fb, k0, m0 + (RAG_M ? ti.row0 : 0), za);
+          }
+          if (B_MN) {
+            tma_load_3d_pair(sb, &tmB, fb, n0, k0, zb);
+            tma_load_3d_pair(sb + kChunkBytes, &tmB, fb, n0 + 64, k0, zb);
+          } else {
+            tma_load_3d_pair(sb, &tmB, fb, k0, n0, zb);
+          }
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (ok) {
+        // the last round's "empty" arrivals land in this CTA's shared memory:
+        // wait for them so that none is still in flight when the CTA exits
+        for (int s = 0; s < kStages; ++s)
+          if (issued & (1u << s)) {
+            int dummy = 0;
+            wait_bounded(empty_bar(s), (issued_parity >> s) & 1u, &dummy, nullptr);
+          }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ----------------------------------------- MMA issuer (leader only) ----
+    if (lane == 0 && leader) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int it = 0;
+      bool ok = true;
+      for (int tile = cluster; tile < total_tiles && ok; tile += nclusters) {
+        const Tile ti = tile_of(tile);
+        if (RAG_K && ti.nkb == 0) continue;  // an empty group: the epilogue writes zeros
+        const int acc = it & 1;
+        const uint32_t ap = (it >> 1) & 1;
+        ++it;
+        if (!wait_bounded(tempty_bar(acc), ap ^ 1u, abort_p, args.status)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTile);
+        for (int kb = 0; kb < ti.nkb; ++kb) {
+          if (!wait_bounded(full_bar(stage), phase, abort_p, args.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_base + stage * kStageBytes;
+          const uint32_t sb = sa + kOpBytes;
+#pragma unroll
+          for (int k = 0; k < kKB / 16; ++k) {
+            // 16 k values: 32 bytes along a K-major row, 16 rows of 128 bytes
+            const uint64_t da = A_MN ? desc_mnmajor_sw128(sa + k * 2048, kChunkBytes)
+                                     : desc_kmajor_sw128(sa + k * 32);
+            const uint64_t db = B_MN ? desc_mnmajor_sw128(sb + k * 2048, kChunkBytes)
+                                     : desc_kmajor_sw128(sb + k * 32);
+            mma_bf16_pair(d_tmem, da, db, IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+          }
+          mma_commit_pair(empty_bar(stage), kBoth);
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+        if (ok) mma_commit_pair(tfull_bar(acc), kBoth);
+      }
+      if (!ok) {
+        // wait for every MMA already issued before TMEM is released
+        mma_commit_pair(drain_bar, 0x1);
+        int dummy = 0;
+        wait_bounded(drain_bar, 0, &dummy, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (RAG_K && warp == 3) {
+    // ------------------------- the last k-block's rows behind the group ----
+    uint32_t parity = 0;  // of each stage's landing barrier
+    int done = 0;         // stage of the next tile's first k-block
+    for (int tile = cluster; tile < total_tiles; tile += nclusters) {
+      const Tile ti = tile_of(tile);
+      const int rem = ti.rows & (kKB - 1);
+      if (rem != 0) {
+        const int s = (done + ti.nkb - 1) % kStages;
+        if (!wait_bounded(land_bar(s), (parity >> s) & 1u, abort_p, args.status)) break;
+        parity ^= 1u << s;
+        uint8_t* base = smem + s * kStageBytes;
+        // rows rem..63 are the tail of each of the four 64-wide slices
+        for (int o = rem * 128 + lane * 16; o < static_cast<int>(kChunkBytes); o += 512) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(base + c * kChunkBytes + o) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_release(map_to_cta(full_bar(s), 0));
+      }
+      done = (done + ti.nkb) % kStages;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------- epilogue -----
+    const int q = warp & 3;            // TMEM lane quarter of this warp
+    const int hcol = (warp - 4) >> 2;  // which half of the tile's columns it drains
+    const int r = q * 32 + lane;
+    const uint32_t tempty_leader0 = map_to_cta(tempty_bar(0), 0);
+    const uint32_t tempty_leader1 = map_to_cta(tempty_bar(1), 0);
+    uint8_t* stage = smem + kStages * kStageBytes + (warp - 4) * kWarpStage;
+    int it = 0;
+    for (int tile = cluster; tile < total_tiles; tile += nclusters) {
+      const Tile ti = tile_of(tile);
+      const bool empty = RAG_K && ti.nkb == 0;
+      const int acc = it & 1;
+      const uint32_t ap = (it >> 1) & 1;
+      if (!empty) {
+        ++it;
+        if (!wait_bounded(tfull_bar(acc), ap, abort_p, args.status)) break;
+        tc_fence_after();
+      }
+      const int row = ti.m_blk * kTile + static_cast<int>(rank) * kHalf + r;
+      const bool live = row < (RAG_K ? args.m : ti.rows);
+      const int col0 = ti.n_blk * kTile + hcol * 128;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                             static_cast<uint32_t>(acc * kTile + hcol * 128);
+      const int64_t orow = RAG_M ? static_cast<int64_t>(ti.row0) + row : row;
+      const int64_t obase = (RAG_M ? 0 : ti.g * args.out_stride) + orow * args.ld;
+      if (EPI == kMmStoreBf16) {
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int col = col0 + c * 64;
+          if (col >= args.n) break;
+          float x[64];
+          if (!empty) {
+            tmem_ld32(taddr + c * 64, x);
+            tmem_ld32(taddr + c * 64 + 32, x + 32);
+            tmem_ld_wait_regs(x);
+            tmem_ld_wait_regs(x + 32);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] = 0.0f;
+          }
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            Vec16<bf16>::store(reinterpret_cast<bf16*>(&v[i]), x + i * 8);
+          bf16* out = static_cast<bf16*>(args.out) + obase + col;
+          store_rows<8>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
+                        (args.n - col) / 8, lane, PutPlain{});
+        }
+      } else if (EPI == kMmStoreF32 || EPI == kMmAddF32) {
+        if (!(EPI == kMmAddF32 && empty)) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const int col = col0 + c * 32;
+            if (col >= args.n) break;
+            float x[32];
+            if (!empty) {
+              tmem_ld32(taddr + c * 32, x);
+              tmem_ld_wait_regs(x);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+            }
+            float* out = static_cast<float*>(args.out) + obase + col;
+            uint8_t* dst = live ? reinterpret_cast<uint8_t*>(out) : nullptr;
+            const uint4* v = reinterpret_cast<const uint4*>(x);
+            if (EPI == kMmAddF32)
+              store_rows<8>(stage, v, dst, (args.n - col) / 4, lane, PutAddF32{});
+            else
+              store_rows<8>(stage, v, dst, (args.n - col) / 4, lane, PutPlain{});
+          }
+        }
+      } else if (EPI == kMmGram || EPI == kMmPoly) {
+        // fp16 off the diagonal, the diagonal itself in fp32 apart
+        const float* diag = EPI == kMmPoly ? args.diag + static_cast<int64_t>(ti.g) * args.diag_ld
+                                           : nullptr;
+        float* dout = args.diag_out + static_cast<int64_t>(ti.g) * args.diag_ld;
+        __half* omat = static_cast<__half*>(args.out) + ti.g * args.out_stride;
+        const float di = EPI == kMmPoly && live ? diag[row] : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = col0 + c * 32;
+          if (col >= args.n) break;
+          float x[32];
+          tmem_ld32(taddr + c * 32, x);
+          tmem_ld_wait_regs(x);
+          if (EPI == kMmGram) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] *= args.inv_scale2;
+          } else {
+            const __half* src = static_cast<const __half*>(args.src) + ti.g * args.out_stride +
+                                static_cast<int64_t>(row) * args.ld + col;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              float a[8];
+              if (live && col + i < args.ld) {
+                unpack_half8(*reinterpret_cast<const uint4*>(src + i), a);
+                const float4 d0 = *reinterpret_cast<const float4*>(diag + col + i);
+                const float4 d1 = *reinterpret_cast<const float4*>(diag + col + i + 4);
+                const float dj[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const bool on = col + i + j == row;
+                  // on the diagonal (a = 0): b d + c (d^2 + o)
+                  const float lin = on ? di : a[j];
+                  const float quad = on ? di * di : (di + dj[j]) * a[j];
+                  x[i + j] = args.cb * lin + args.cc * (quad + x[i + j]);
+                }
+              }
+            }
+          }
+          if (live && row >= col && row < col + 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col + i == row) {
+                dout[row] = x[i];
+                x[i] = 0.0f;
+              }
+          }
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = pack_half8(x + i * 8);
+          __half* out = omat + static_cast<int64_t>(row) * args.ld + col;
+          store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
+                        static_cast<int>(args.ld - col) / 8, lane, PutPlain{});
+          if (SYM && ti.m_blk != ti.n_blk && live) {
+            // the mirrored tile: consecutive lanes hold consecutive columns
+            __half* mir = omat + static_cast<int64_t>(col) * args.ld + row;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col + i < args.n) mir[static_cast<int64_t>(i) * args.ld] = __float2half_rn(x[i]);
+          }
+        }
+      } else {
+        // X' = a (hi + lo) + d hi + (B off its diagonal) hi, all times `scale`
+        const float* diag = args.diag + static_cast<int64_t>(ti.g) * args.diag_ld;
+        const int64_t src_stride = static_cast<int64_t>(args.m) * args.ld;
+        const float drow = !args.diag_cols && live ? diag[row] : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = col0 + c * 32;
+          if (col >= args.n) break;
+          float x[32];
+          tmem_ld32(taddr + c * 32, x);
+          tmem_ld_wait_regs(x);
+          const int64_t at = ti.g * src_stride + static_cast<int64_t>(row) * args.ld + col;
+          const __half* hi = static_cast<const __half*>(args.src) + at;
+          const __half* lo = static_cast<const __half*>(args.src_lo) + at;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            if (live && col + i < args.ld) {
+              float h[8], l[8];
+              unpack_half8(*reinterpret_cast<const uint4*>(hi + i), h);
+              unpack_half8(*reinterpret_cast<const uint4*>(lo + i), l);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float d =
+                    args.diag_cols ? (col + i + j < args.n ? diag[col + i + j] : 0.0f) : drow;
+                x[i + j] = args.ca * (h[j] + l[j]) + d * h[j] + x[i + j];
+              }
+            }
+          }
+          if (args.out_lo != nullptr) {
+            float l[32];
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = pack_half8(x + i * 8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float h[8];
+              unpack_half8(v[i], h);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) l[i * 8 + j] = x[i * 8 + j] - h[j];
+            }
+            const int pieces = static_cast<int>(args.ld - col) / 8;
+            __half* o = static_cast<__half*>(args.out) + at;
+            store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(o) : nullptr, pieces, lane,
+                          PutPlain{});
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = pack_half8(l + i * 8);
+            o = static_cast<__half*>(args.out_lo) + at;
+            store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(o) : nullptr, pieces, lane,
+                          PutPlain{});
+          } else {
+            // the last step: bf16 in the caller's dense layout
+            const float inv = 1.0f / args.scale;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] *= inv;
+            bf16* out = static_cast<bf16*>(args.out) + ti.g * args.out_stride +
+                        static_cast<int64_t>(row) * args.n + col;
+            if (args.vec_ok) {
+              uint4 v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                Vec16<bf16>::store(reinterpret_cast<bf16*>(&v[i]), x + i * 8);
+              store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
+                            (args.n - col) / 8, lane, PutPlain{});
+            } else if (live) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (col + i < args.n) out[i] = __float2bfloat16_rn(x[i]);
+            }
+          }
+        }
+      }
+      if (!empty) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();  // no CTA of the pair leaves while the other still works
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+template <int LAYOUT, int SCHED, int EPI, bool FP16>
+int launch_impl(const CUtensorMap& a, const CUtensorMap& b, const MmArgs& args, int pairs,
+                cudaStream_t st) {
+  static std::atomic<uint64_t> optin{0};
+  auto kern = mm_pair_kernel<LAYOUT, SCHED, EPI, FP16>;
+  if (int rc = ensure_smem_optin(reinterpret_cast<const void*>(kern), kSmemBytes, optin)) return rc;
+  return launch_k(kern, dim3(2 * pairs), kThreads, kSmemBytes, st, 2, a, b, args);
+}
+
+}  // namespace
+
+bool make_map_16bit(CUtensorMap* map, bool fp16, const void* base, uint64_t inner, uint64_t rows,
+                    uint64_t depth, uint64_t ld, uint64_t stride, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn || !base || inner == 0 || rows == 0 || depth == 0) return false;
+  cuuint64_t dims[3] = {inner, rows, depth};
+  cuuint64_t strides[2] = {ld * 2, stride * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int launch_mm(int layout, int sched, int epi, const CUtensorMap& a, const CUtensorMap& b,
+              const MmArgs& args, int pairs, cudaStream_t st) {
+  if (pairs <= 0) return MOE_OK;
+  if (sched == kMmRaggedM && epi == kMmStoreBf16) {
+    if (layout == kMmNT) return launch_impl<kMmNT, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
+    if (layout == kMmNN) return launch_impl<kMmNN, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
+  }
+  if (sched == kMmRaggedK && layout == kMmTN) {
+    if (epi == kMmStoreBf16) return launch_impl<kMmTN, kMmRaggedK, kMmStoreBf16, false>(a, b, args, pairs, st);
+    if (epi == kMmStoreF32) return launch_impl<kMmTN, kMmRaggedK, kMmStoreF32, false>(a, b, args, pairs, st);
+    if (epi == kMmAddF32) return launch_impl<kMmTN, kMmRaggedK, kMmAddF32, false>(a, b, args, pairs, st);
+  }
+  if (sched == kMmBatchSym && epi == kMmGram) {
+    if (layout == kMmNT) return launch_impl<kMmNT, kMmBatchSym, kMmGram, true>(a, b, args, pairs, st);
+    if (layout == kMmTN) return launch_impl<kMmTN, kMmBatchSym, kMmGram, true>(a, b, args, pairs, st);
+  }
+  if (sched == kMmBatchSym && epi == kMmPoly && layout == kMmNT)
+    return launch_impl<kMmNT, kMmBatchSym, kMmPoly, true>(a, b, args, pairs, st);
+  if (sched == kMmBatch && epi == kMmUpdate) {
+    if (layout == kMmNT) return launch_impl<kMmNT, kMmBatch, kMmUpdate, true>(a, b, args, pairs, st);
+    if (layout == kMmNN) return launch_impl<kMmNN, kMmBatch, kMmUpdate, true>(a, b, args, pairs, st);
+  }
+  return MOE_ERR_SHAPE;
+}
+
+}  // namespace sm100
+}  // namespace moe

@@ -1,0 +1,78 @@
+// Host interface of the tcgen05 matrix products of the training operators
+// (mm_sm100.cu): products of ragged row groups with their group's matrix, and
+// the products of the Newton-Schulz iteration over a stack of matrices.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+namespace sm100 {
+
+// Operand layouts of D[M, N] = sum_k A(m, k) B(n, k).  K-major: k runs along
+// the memory rows; MN-major: m (or n) does.
+enum MmLayout {
+  kMmNT = 0,  // A [M, K], B [N, K]: both K-major
+  kMmNN = 1,  // A [M, K] K-major, B [K, N] MN-major
+  kMmTN = 2,  // A [K, M], B [K, N]: both MN-major
+};
+
+// What a tile's rows, columns and reduction come from.
+enum MmSched {
+  kMmRaggedM = 0,  // rows offsets[g] .. offsets[g+1]-1 against matrix g
+  kMmRaggedK = 1,  // the reduction runs over those rows; one output per group
+  kMmBatch = 2,    // `groups` equal products
+  kMmBatchSym = 3, // the same, D symmetric: only tiles on or below the diagonal
+};
+
+enum MmEpi {
+  kMmStoreBf16 = 0,
+  kMmStoreF32 = 1,
+  kMmAddF32 = 2,   // out += D
+  kMmGram = 3,     // Newton-Schulz: A = X X^T, diagonal apart
+  kMmPoly = 4,     // Newton-Schulz: B = b A + c A A, diagonal apart
+  kMmUpdate = 5,   // Newton-Schulz: X <- a X + B X
+};
+
+constexpr int kMmMaxGroups = 256;
+
+struct MmArgs {
+  const int32_t* offsets;  // ragged schedules: device, [groups + 1]
+  int32_t rows;            // ragged schedules: bound of the offsets
+  int32_t groups;
+  int32_t m;               // rows of D of one group (not kMmRaggedM)
+  int32_t n;               // columns of D
+  int32_t k;               // reduction length (not kMmRaggedK)
+  void* out;
+  int64_t ld;              // elements between rows of out
+  int64_t out_stride;      // elements between groups of out (not kMmRaggedM)
+  int32_t* status;
+  // Newton-Schulz only; see ortho.cu for what each holds
+  const void* src;         // kMmPoly: A off the diagonal; kMmUpdate: X, high part
+  const void* src_lo;      // kMmUpdate: X, low part
+  void* out_lo;            // kMmUpdate: X', low part (NULL: the last step)
+  const float* diag;       // kMmPoly: diagonal of A; kMmUpdate: diagonal of B
+  float* diag_out;         // kMmGram, kMmPoly
+  int32_t diag_ld;         // elements between matrices of diag
+  int32_t diag_cols;       // kMmUpdate: B stands on the right (its diagonal scales columns)
+  int32_t vec_ok;          // kMmUpdate, last step: rows of out are 16-byte aligned
+  float ca, cb, cc;        // coefficients of the step
+  float scale, inv_scale2; // X is held times `scale`; 1 / scale^2
+};
+
+// Rank-3 map {inner, rows, depth} with 128-byte swizzle and box {64, box_rows, 1}
+// of a 16-bit type; strides in elements.
+bool make_map_16bit(CUtensorMap* map, bool fp16, const void* base, uint64_t inner, uint64_t rows,
+                    uint64_t depth, uint64_t ld, uint64_t stride, uint32_t box_rows);
+
+// Box rows of the A (or B) map of a layout: 128 rows K-major, 64 MN-major.
+inline uint32_t mm_box_a(int layout) { return layout == kMmTN ? 64u : 128u; }
+inline uint32_t mm_box_b(int layout) { return layout == kMmNT ? 128u : 64u; }
+
+// `pairs` CTA pairs compute the product.
+int launch_mm(int layout, int sched, int epi, const CUtensorMap& a, const CUtensorMap& b,
+              const MmArgs& args, int pairs, cudaStream_t st);
+
+}  // namespace sm100
+}  // namespace moe

@@ -13,6 +13,22 @@ __device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_add
                : "memory");
 }
 
+// One lane of a converged warp.  The issuing warps run their loops with all
+// lanes and pick one for the TMA and MMA instructions only: those take their
+// operands from uniform registers, and inside a branch on the lane number the
+// compiler cannot tell that a value is uniform (MMA issue then bounds the
+// kernel: with it, 0.45 us per 64-wide k-block).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Shared-memory matrix descriptor for an MN-major operand tile written by TMA
 // with 128-byte swizzling: slices of 64 m (or n) values in k rows of 128
 // bytes, groups of 8 k rows 1024 B apart, the next slice `slice_bytes` on.

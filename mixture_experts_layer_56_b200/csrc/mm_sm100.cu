@@ -11,9 +11,9 @@
 // box holds 64 k rows of one 64-wide slice, and the MMA's descriptor and the
 // instruction's major bit say so.
 //
-// A tile is 256 x 256, its rows split over the two SMs of a cluster: each CTA
+// A tile is 256 x 256 at most, its rows split over the two SMs of a cluster: each CTA
 // loads its 128 rows of A and its half of B's 256 rows, and the leader issues
-// M = 256, N = 256 MMAs for both.  Six 32 KB stages per CTA; the accumulator
+// M = 256, N = 256 MMAs for both.  Five 32 KB stages per CTA; the accumulator
 // is double-buffered in TMEM (2 x 256 columns), so that the epilogue of one
 // tile runs under the MMAs of the next.  Warps: 0 TMA, 1 MMA, 2 TMEM, 3 the
 // ragged reduction's zeroing, 4-11 epilogue.
@@ -39,19 +39,28 @@ namespace sm100 {
 
 namespace {
 
-constexpr int kTile = 256;      // rows and columns of a pair's tile
-constexpr int kHalf = 128;      // rows of A, and of B, per CTA
+constexpr int kTile = 256;      // rows, and most columns, of a pair's tile
+constexpr int kHalf = 128;      // rows of a tile per CTA
 constexpr int kKB = 64;         // k-block
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kStagePitch = 128 + 16;  // staging row: 128 bytes, padded off the bank period
 constexpr int kWarpStage = 32 * kStagePitch;
-constexpr uint32_t kOpBytes = kHalf * kKB * 2;       // one operand of a stage
-constexpr uint32_t kStageBytes = 2 * kOpBytes;
-constexpr uint32_t kChunkBytes = 64 * kKB * 2;       // an MN-major 64-wide slice
-constexpr int kStages = 5;
-constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kWarpStage + 1024;
+constexpr uint32_t kSliceBytes = 64 * kKB * 2;  // an MN-major 64-wide slice
 constexpr int kColChunk = 8;  // N tiles that a group's row blocks sweep together
+
+// Shared memory with AR rows of A in a stage.
+template <int AR>
+struct Stage {
+  static constexpr uint32_t kA = AR * kKB * 2;
+  static constexpr uint32_t kB = kHalf * kKB * 2;
+  static constexpr uint32_t kBytes = kA + kB;
+  // what 227 KB hold beside the epilogue's staging and 5 KB of barriers,
+  // group tables and alignment
+  static constexpr int kCount = (227 * 1024 - 5120 - kEpiWarps * kWarpStage) / kBytes;
+  static constexpr int kSmem = kCount * kBytes + kEpiWarps * kWarpStage + 1024;
+  static_assert(kCount >= 4 && kCount <= 16, "the issued-stage masks hold 32");
+};
 
 // Rows of 32 lanes (lane r holds row r, NV 16-byte pieces) written to global
 // memory as whole row segments through the warp's staging area.  `dst` is the
@@ -76,6 +85,30 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint4* v, uint8
   }
   __syncwarp();
 }
+
+// The other way round: a warp's 32 rows of 64 bytes (32 fp16 values), read as
+// whole row segments.  fetch() starts the loads (rows at or past `rows` and
+// pieces past the matrix give zeros), put() leaves row r's bytes at
+// stage + r * kStagePitch + offset for lane r.
+struct RowFetch {
+  uint4 v[4];
+  __device__ __forceinline__ void fetch(const __half* base, int64_t ld, int rows, int pieces,
+                                        int lane) {
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int row = it * 8 + lane / 4, c = lane % 4;
+      v[it] = row < rows && c < pieces
+                  ? *reinterpret_cast<const uint4*>(base + row * ld + c * 8)
+                  : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void put(uint8_t* stage, int offset, int lane) const {
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+      *reinterpret_cast<uint4*>(stage + (it * 8 + lane / 4) * kStagePitch + offset +
+                                (lane % 4) * 16) = v[it];
+  }
+};
 
 struct PutPlain {
   __device__ __forceinline__ void operator()(uint4* p, uint4 x) const { *p = x; }
@@ -112,10 +145,13 @@ struct Tile {
   int g, m_blk, n_blk;
   int row0;  // ragged: the group's first row
   int rows;  // rows of D of the group (ragged rows, or m), or the ragged reduction's length
+  int len;   // of the reduction
   int nkb;   // k-blocks
+  int col0;  // first column of D
+  int ncols; // of the MMA
 };
 
-template <int LAYOUT, int SCHED, int EPI, bool FP16>
+template <int LAYOUT, int SCHED, int EPI, bool FP16, int AR>
 __global__ void __launch_bounds__(kThreads, 1)
 mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const MmArgs args) {
@@ -124,28 +160,33 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   constexpr bool RAG_M = SCHED == kMmRaggedM;
   constexpr bool RAG_K = SCHED == kMmRaggedK;
   constexpr bool SYM = SCHED == kMmBatchSym;
-  constexpr uint32_t IDESC = idesc_16bit_f32(kTile, kTile, FP16, A_MN, B_MN);
+  constexpr uint32_t A_BYTES = Stage<AR>::kA;
+  constexpr uint32_t B_BYTES = Stage<AR>::kB;
+  constexpr uint32_t STAGE_BYTES = Stage<AR>::kBytes;
+  constexpr int STAGES = Stage<AR>::kCount;
   constexpr uint32_t TMEM_COLS = 2 * kTile;
+  static_assert(!A_MN || AR == 128, "an MN-major A comes in two slices");
   constexpr uint16_t kBoth = 0x3;
 
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[3 * kStages + 5];
+  __shared__ __align__(8) uint64_t bars[3 * STAGES + 5];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ int32_t tile_start[kMmMaxGroups + 1];
   __shared__ int32_t grp_row0[kMmMaxGroups];
   __shared__ int32_t grp_rows[kMmMaxGroups];
+  __shared__ int16_t grp_order[kMmMaxGroups];  // ragged reductions: longest first
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t smem_base = smem_addr(smem);
   const uint32_t bar_base = smem_addr(bars);
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
-  auto empty_bar = [&](int s) { return bar_base + 8u * (kStages + s); };
-  auto land_bar = [&](int s) { return bar_base + 8u * (2 * kStages + s); };
-  auto tfull_bar = [&](int a) { return bar_base + 8u * (3 * kStages + a); };
-  auto tempty_bar = [&](int a) { return bar_base + 8u * (3 * kStages + 2 + a); };
-  const uint32_t drain_bar = bar_base + 8u * (3 * kStages + 4);
+  auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+  auto land_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (3 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (3 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar_base + 8u * (3 * STAGES + 4);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -155,12 +196,13 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int cluster = static_cast<int>(cluster_id_x());
   const int nclusters = static_cast<int>(num_clusters_x());
   const int G = args.groups;
-  const int nt = (args.n + kTile - 1) / kTile;
+  const int tn = args.tn;  // columns of a tile
+  const int nt = (args.n + tn - 1) / tn;
   volatile int* abort_p = &abort_flag;
 
   // ---- setup --------------------------------------------------------------
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       // the leader's arrive (+ both CTAs' bytes); with a ragged reduction
       // either CTA arrives, its rows zeroed where the k-block is a group's last
       mbar_init(full_bar(s), RAG_K ? 2 : 1);
@@ -193,6 +235,15 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       tile_start[g + 1] = ((b - a + kTile - 1) / kTile) * nt;
     }
     __syncthreads();
+    if (RAG_K) {
+      // tiles of equal length run side by side, the longest first
+      for (int g = tid; g < G; g += kThreads) {
+        int before = 0;
+        for (int i = 0; i < G; ++i)
+          before += grp_rows[i] > grp_rows[g] || (grp_rows[i] == grp_rows[g] && i < g);
+        grp_order[before] = static_cast<int16_t>(g);
+      }
+    }
     if (RAG_M && warp == 0) {
       const int per = (G + 31) / 32;
       const int beg = min(lane * per, G);
@@ -221,8 +272,18 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int per_group = SYM ? mt_fixed * (mt_fixed + 1) / 2 : mt_fixed * nt;
   const int total_tiles = RAG_M ? tile_start[G] : G * per_group;
 
-  auto tile_of = [&](int t) {
+  // position v of this pair's sequence cluster, cluster + nclusters, ...
+  auto tile_of = [&](int v) {
     Tile ti;
+    int t = v;
+    if (RAG_K) {
+      // Every other round backwards: a round's tiles get shorter from first
+      // to last, and so no pair has the longer one of every round.
+      const int round = v / nclusters;
+      const int first = round * nclusters;
+      const int here = min(nclusters, total_tiles - first);
+      if (round & 1) t = first + here - 1 - (v - first);
+    }
     if (RAG_M) {
       int lo = 0, hi = G - 1;
       while (lo < hi) {
@@ -242,10 +303,10 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       ti.n_blk = c * cw + (rem - ti.m_blk * wc);
       ti.row0 = grp_row0[lo];
       ti.rows = grp_rows[lo];
-      ti.nkb = (args.k + kKB - 1) / kKB;
     } else {
       ti.g = t / per_group;
       const int local = t - ti.g * per_group;
+      if (RAG_K) ti.g = grp_order[ti.g];
       if (SYM) {
         int mb = static_cast<int>((sqrtf(8.0f * local + 1.0f) - 1.0f) * 0.5f);
         while (mb * (mb + 1) / 2 > local) --mb;
@@ -258,8 +319,31 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       }
       ti.row0 = RAG_K ? grp_row0[ti.g] : 0;
       ti.rows = RAG_K ? grp_rows[ti.g] : args.m;
-      ti.nkb = ((RAG_K ? ti.rows : args.k) + kKB - 1) / kKB;
     }
+    ti.len = RAG_K ? ti.rows : args.k;
+    ti.nkb = (ti.len + kKB - 1) / kKB;
+    ti.col0 = ti.n_blk * tn;
+    // the MMA's width: the last column tile's, in steps of 32
+    ti.ncols = min(tn, (args.n - ti.col0 + 31) & ~31);
+    return ti;
+  };
+  // whether CTA `r` of the pair has rows in the tile
+  auto has_rows = [&](const Tile& ti, int r) {
+    return ti.m_blk * kTile + r * kHalf < (RAG_K ? args.m : ti.rows);
+  };
+
+  // the same with every field known to be uniform across the warp
+  auto uniform_tile = [&](int v) {
+    Tile ti = tile_of(v);
+    ti.g = uniform(ti.g);
+    ti.m_blk = uniform(ti.m_blk);
+    ti.n_blk = uniform(ti.n_blk);
+    ti.row0 = uniform(ti.row0);
+    ti.rows = uniform(ti.rows);
+    ti.len = uniform(ti.len);
+    ti.nkb = uniform(ti.nkb);
+    ti.col0 = uniform(ti.col0);
+    ti.ncols = uniform(ti.ncols);
     return ti;
   };
 
@@ -268,98 +352,124 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (lane == 0) {
       tma_prefetch_desc(&tmA);
       tma_prefetch_desc(&tmB);
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_parity = 0;
-      bool ok = true;
-      for (int tile = cluster; tile < total_tiles && ok; tile += nclusters) {
-        const Tile ti = tile_of(tile);
-        const int m0 = ti.m_blk * kTile + static_cast<int>(rank) * kHalf;
-        const int n0 = ti.n_blk * kTile + static_cast<int>(rank) * kHalf;
-        const int za = RAG_M || RAG_K ? 0 : ti.g;
-        const int zb = RAG_K ? 0 : ti.g;
-        for (int kb = 0; kb < ti.nkb; ++kb) {
-          if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_p, args.status)) { ok = false; break; }
-          const uint32_t sa = smem_base + stage * kStageBytes;
-          const uint32_t sb = sa + kOpBytes;
-          // a ragged group's last, partial k-block lands on this CTA's own
-          // barrier, where warp 3 takes it over
-          const bool partial = RAG_K && kb == ti.nkb - 1 && (ti.rows & (kKB - 1)) != 0;
-          uint32_t fb;
-          if (partial) {
-            fb = land_bar(stage);
-            mbar_arrive_expect_tx(fb, kStageBytes);
-          } else {
-            fb = leader ? full_bar(stage) : map_to_cta(full_bar(stage), 0);
-            if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);
-            else if (RAG_K) mbar_arrive_cluster(fb);
-          }
-          const int k0 = kb * kKB + (RAG_K ? ti.row0 : 0);
-          if (A_MN) {
-            tma_load_3d_pair(sa, &tmA, fb, m0, k0, za);
-            tma_load_3d_pair(sa + kChunkBytes, &tmA, fb, m0 + 64, k0, za);
-          } else {
-            tma_load_3d_pair(sa, &tmA, fb, k0, m0 + (RAG_M ? ti.row0 : 0), za);
+    }
+    __syncwarp();
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_parity = 0;
+    bool ok = true;
+    for (int tile = cluster; tile < total_tiles && ok; tile += nclusters) {
+      const Tile ti = uniform_tile(tile);
+      const int m0 = ti.m_blk * kTile + static_cast<int>(rank) * kHalf + (RAG_M ? ti.row0 : 0);
+      const int n0 = ti.col0 + static_cast<int>(rank) * (ti.ncols / 2);
+      // a CTA without rows leaves its part of A as it is: what the MMA makes
+      // of it is not stored
+      const bool mine = has_rows(ti, static_cast<int>(rank));
+      const uint32_t bytes = (mine ? A_BYTES : 0) + B_BYTES;
+      const uint32_t pair_bytes = 2 * B_BYTES + A_BYTES + (has_rows(ti, 1) ? A_BYTES : 0);
+      const int za = RAG_M || RAG_K ? 0 : ti.g;
+      const int zb = RAG_K ? 0 : ti.g;
+      int k0 = RAG_K ? ti.row0 : 0;
+      for (int kb = 0; kb < ti.nkb; ++kb, k0 += kKB) {
+        ok = __all_sync(0xffffffffu,
+                        wait_bounded(empty_bar(stage), phase ^ 1u, abort_p, args.status));
+        if (!ok) break;
+        const uint32_t sa = smem_base + stage * STAGE_BYTES;
+        const uint32_t sb = sa + A_BYTES;
+        // a ragged group's last, partial k-block lands on this CTA's own
+        // barrier, where warp 3 takes it over
+        const bool partial = RAG_K && kb == ti.nkb - 1 && (ti.rows & (kKB - 1)) != 0;
+        const uint32_t fb = partial || leader ? (partial ? land_bar(stage) : full_bar(stage))
+                                              : map_to_cta(full_bar(stage), 0);
+        if (elect_lane()) {
+          if (partial) mbar_arrive_expect_tx(fb, bytes);
+          else if (leader) mbar_arrive_expect_tx(fb, pair_bytes);
+          else if (RAG_K) mbar_arrive_cluster(fb);
+          if (mine) {
+            if (A_MN) {
+              tma_load_3d_pair(sa, &tmA, fb, m0, k0, za);
+              tma_load_3d_pair(sa + kSliceBytes, &tmA, fb, m0 + 64, k0, za);
+            } else {
+              tma_load_3d_pair(sa, &tmA, fb, k0, m0, za);
+            }
           }
           if (B_MN) {
             tma_load_3d_pair(sb, &tmB, fb, n0, k0, zb);
-            tma_load_3d_pair(sb + kChunkBytes, &tmB, fb, n0 + 64, k0, zb);
+            tma_load_3d_pair(sb + kSliceBytes, &tmB, fb, n0 + 64, k0, zb);
           } else {
             tma_load_3d_pair(sb, &tmB, fb, k0, n0, zb);
           }
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
+        __syncwarp();
+        issued |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      if (ok) {
-        // the last round's "empty" arrivals land in this CTA's shared memory:
-        // wait for them so that none is still in flight when the CTA exits
-        for (int s = 0; s < kStages; ++s)
-          if (issued & (1u << s)) {
-            int dummy = 0;
-            wait_bounded(empty_bar(s), (issued_parity >> s) & 1u, &dummy, nullptr);
-          }
-      }
+    }
+    if (ok) {
+      // the last round's "empty" arrivals land in this CTA's shared memory:
+      // wait for them so that none is still in flight when the CTA exits
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) {
+          int dummy = 0;
+          wait_bounded(empty_bar(s), (issued_parity >> s) & 1u, &dummy, nullptr);
+        }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------- MMA issuer (leader only) ----
-    if (lane == 0 && leader) {
+    if (leader) {
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
       bool ok = true;
       for (int tile = cluster; tile < total_tiles && ok; tile += nclusters) {
-        const Tile ti = tile_of(tile);
+        const Tile ti = uniform_tile(tile);
         if (RAG_K && ti.nkb == 0) continue;  // an empty group: the epilogue writes zeros
         const int acc = it & 1;
         const uint32_t ap = (it >> 1) & 1;
         ++it;
-        if (!wait_bounded(tempty_bar(acc), ap ^ 1u, abort_p, args.status)) { ok = false; break; }
+        ok = __all_sync(0xffffffffu,
+                        wait_bounded(tempty_bar(acc), ap ^ 1u, abort_p, args.status));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kTile);
+        const uint32_t idesc = idesc_16bit_f32(kTile, 0, FP16, A_MN, B_MN) |
+                               (static_cast<uint32_t>(ti.ncols >> 3) << 17);
         for (int kb = 0; kb < ti.nkb; ++kb) {
-          if (!wait_bounded(full_bar(stage), phase, abort_p, args.status)) { ok = false; break; }
+          ok = __all_sync(0xffffffffu, wait_bounded(full_bar(stage), phase, abort_p, args.status));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_base + stage * kStageBytes;
-          const uint32_t sb = sa + kOpBytes;
+          // 16 k values further: 32 bytes along a K-major row, 16 rows of 128
+          // bytes of an MN-major slice
+          const uint32_t sa = smem_base + stage * STAGE_BYTES;
+          const uint64_t da = A_MN ? desc_mnmajor_sw128(sa, kSliceBytes) : desc_kmajor_sw128(sa);
+          const uint64_t db = B_MN ? desc_mnmajor_sw128(sa + A_BYTES, kSliceBytes)
+                                   : desc_kmajor_sw128(sa + A_BYTES);
+          constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
+          // steps of 16 that hold anything of the reduction
+          const int steps = min(kKB, ti.len - kb * kKB + 15) >> 4;
+          if (elect_lane()) {
+            if (steps == 4) {
 #pragma unroll
-          for (int k = 0; k < kKB / 16; ++k) {
-            // 16 k values: 32 bytes along a K-major row, 16 rows of 128 bytes
-            const uint64_t da = A_MN ? desc_mnmajor_sw128(sa + k * 2048, kChunkBytes)
-                                     : desc_kmajor_sw128(sa + k * 32);
-            const uint64_t db = B_MN ? desc_mnmajor_sw128(sb + k * 2048, kChunkBytes)
-                                     : desc_kmajor_sw128(sb + k * 32);
-            mma_bf16_pair(d_tmem, da, db, IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_pair(d_tmem, da + k * a_step, db + k * b_step, idesc,
+                              (kb > 0 || k > 0) ? 1u : 0u);
+            } else {
+              for (int k = 0; k < steps; ++k)
+                mma_bf16_pair(d_tmem, da + k * a_step, db + k * b_step, idesc,
+                              (kb > 0 || k > 0) ? 1u : 0u);
+            }
+            mma_commit_pair(empty_bar(stage), kBoth);
+            if (kb == ti.nkb - 1) mma_commit_pair(tfull_bar(acc), kBoth);
           }
-          mma_commit_pair(empty_bar(stage), kBoth);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+          __syncwarp();
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (ok) mma_commit_pair(tfull_bar(acc), kBoth);
       }
       if (!ok) {
         // wait for every MMA already issued before TMEM is released
-        mma_commit_pair(drain_bar, 0x1);
+        if (elect_lane()) mma_commit_pair(drain_bar, 0x1);
+        __syncwarp();
         int dummy = 0;
         wait_bounded(drain_bar, 0, &dummy, nullptr);
       }
@@ -373,21 +483,21 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const Tile ti = tile_of(tile);
       const int rem = ti.rows & (kKB - 1);
       if (rem != 0) {
-        const int s = (done + ti.nkb - 1) % kStages;
+        const int s = (done + ti.nkb - 1) % STAGES;
         if (!wait_bounded(land_bar(s), (parity >> s) & 1u, abort_p, args.status)) break;
         parity ^= 1u << s;
-        uint8_t* base = smem + s * kStageBytes;
+        uint8_t* base = smem + s * STAGE_BYTES;
         // rows rem..63 are the tail of each of the four 64-wide slices
-        for (int o = rem * 128 + lane * 16; o < static_cast<int>(kChunkBytes); o += 512) {
+        for (int o = rem * 128 + lane * 16; o < static_cast<int>(kSliceBytes); o += 512) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(base + c * kChunkBytes + o) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(base + c * kSliceBytes + o) = make_uint4(0, 0, 0, 0);
         }
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_release(map_to_cta(full_bar(s), 0));
       }
-      done = (done + ti.nkb) % kStages;
+      done = (done + ti.nkb) % STAGES;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------- epilogue -----
@@ -396,10 +506,41 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int r = q * 32 + lane;
     const uint32_t tempty_leader0 = map_to_cta(tempty_bar(0), 0);
     const uint32_t tempty_leader1 = map_to_cta(tempty_bar(1), 0);
-    uint8_t* stage = smem + kStages * kStageBytes + (warp - 4) * kWarpStage;
+    uint8_t* stage = smem + STAGES * STAGE_BYTES + (warp - 4) * kWarpStage;
     int it = 0;
+    // Newton-Schulz: the values of src beside the accumulator, read two chunks
+    // of 32 columns ahead, across tiles
+    constexpr bool SRC = EPI == kMmPoly || EPI == kMmUpdate;
+    RowFetch src_hi[2], src_lo[2];
+    auto fetch_src = [&](const Tile& t, int c) {
+      const int col = t.col0 + hcol * 128 + c * 32;
+      const int row0 = t.m_blk * kTile + static_cast<int>(rank) * kHalf + q * 32;
+      const int64_t at = t.g * (static_cast<int64_t>(args.m) * args.ld) + row0 * args.ld + col;
+      const int rows = col < t.col0 + tn ? args.m - row0 : 0;
+      const int pieces = (static_cast<int>(args.ld) - col) / 8;
+      src_hi[c & 1].fetch(static_cast<const __half*>(args.src) + at, args.ld, rows, pieces, lane);
+      if (EPI == kMmUpdate)
+        src_lo[c & 1].fetch(static_cast<const __half*>(args.src_lo) + at, args.ld, rows, pieces,
+                            lane);
+    };
+    Tile following{};
+    if (SRC && cluster < total_tiles) {
+      following = tile_of(cluster);
+      fetch_src(following, 0);
+      fetch_src(following, 1);
+    }
     for (int tile = cluster; tile < total_tiles; tile += nclusters) {
-      const Tile ti = tile_of(tile);
+      const Tile ti = SRC ? following : tile_of(tile);
+      const bool more = tile + nclusters < total_tiles;
+      if (SRC && more) following = tile_of(tile + nclusters);
+      // puts chunk c of src into the staging area and fetches the one after next
+      auto take_src = [&](int c) {
+        src_hi[c & 1].put(stage, 0, lane);
+        if (EPI == kMmUpdate) src_lo[c & 1].put(stage, 64, lane);
+        __syncwarp();
+        if (c < 2) fetch_src(ti, c + 2);
+        else if (more) fetch_src(following, c - 2);
+      };
       const bool empty = RAG_K && ti.nkb == 0;
       const int acc = it & 1;
       const uint32_t ap = (it >> 1) & 1;
@@ -410,7 +551,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       }
       const int row = ti.m_blk * kTile + static_cast<int>(rank) * kHalf + r;
       const bool live = row < (RAG_K ? args.m : ti.rows);
-      const int col0 = ti.n_blk * kTile + hcol * 128;
+      const int col0 = ti.col0 + hcol * 128;
+      const int col_end = min(ti.col0 + tn, args.n);
+      const int ld_end = col_end < args.n ? col_end : static_cast<int>(args.ld);
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(acc * kTile + hcol * 128);
       const int64_t orow = RAG_M ? static_cast<int64_t>(ti.row0) + row : row;
@@ -419,7 +562,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           const int col = col0 + c * 64;
-          if (col >= args.n) break;
+          if (col >= col_end) break;
           float x[64];
           if (!empty) {
             tmem_ld32(taddr + c * 64, x);
@@ -436,14 +579,14 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             Vec16<bf16>::store(reinterpret_cast<bf16*>(&v[i]), x + i * 8);
           bf16* out = static_cast<bf16*>(args.out) + obase + col;
           store_rows<8>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
-                        (args.n - col) / 8, lane, PutPlain{});
+                        (col_end - col) / 8, lane, PutPlain{});
         }
       } else if (EPI == kMmStoreF32 || EPI == kMmAddF32) {
         if (!(EPI == kMmAddF32 && empty)) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             const int col = col0 + c * 32;
-            if (col >= args.n) break;
+            if (col >= col_end) break;
             float x[32];
             if (!empty) {
               tmem_ld32(taddr + c * 32, x);
@@ -456,9 +599,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             uint8_t* dst = live ? reinterpret_cast<uint8_t*>(out) : nullptr;
             const uint4* v = reinterpret_cast<const uint4*>(x);
             if (EPI == kMmAddF32)
-              store_rows<8>(stage, v, dst, (args.n - col) / 4, lane, PutAddF32{});
+              store_rows<8>(stage, v, dst, (col_end - col) / 4, lane, PutAddF32{});
             else
-              store_rows<8>(stage, v, dst, (args.n - col) / 4, lane, PutPlain{});
+              store_rows<8>(stage, v, dst, (col_end - col) / 4, lane, PutPlain{});
           }
         }
       } else if (EPI == kMmGram || EPI == kMmPoly) {
@@ -468,10 +611,11 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         float* dout = args.diag_out + static_cast<int64_t>(ti.g) * args.diag_ld;
         __half* omat = static_cast<__half*>(args.out) + ti.g * args.out_stride;
         const float di = EPI == kMmPoly && live ? diag[row] : 0.0f;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int col = col0 + c * 32;
-          if (col >= args.n) break;
+          if (SRC) take_src(c);
+          if (col >= col_end) continue;
           float x[32];
           tmem_ld32(taddr + c * 32, x);
           tmem_ld_wait_regs(x);
@@ -479,32 +623,27 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] *= args.inv_scale2;
           } else {
-            const __half* src = static_cast<const __half*>(args.src) + ti.g * args.out_stride +
-                                static_cast<int64_t>(row) * args.ld + col;
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               float a[8];
-              if (live && col + i < args.ld) {
-                unpack_half8(*reinterpret_cast<const uint4*>(src + i), a);
+              unpack_half8(*reinterpret_cast<const uint4*>(stage + lane * kStagePitch + i * 2), a);
+              if (col + i < args.ld) {
                 const float4 d0 = *reinterpret_cast<const float4*>(diag + col + i);
                 const float4 d1 = *reinterpret_cast<const float4*>(diag + col + i + 4);
                 const float dj[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const bool on = col + i + j == row;
-                  // on the diagonal (a = 0): b d + c (d^2 + o)
-                  const float lin = on ? di : a[j];
-                  const float quad = on ? di * di : (di + dj[j]) * a[j];
-                  x[i + j] = args.cb * lin + args.cc * (quad + x[i + j]);
-                }
+                for (int j = 0; j < 8; ++j)
+                  x[i + j] = args.cb * a[j] + args.cc * ((di + dj[j]) * a[j] + x[i + j]);
               }
             }
+            __syncwarp();
           }
           if (live && row >= col && row < col + 32) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (col + i == row) {
-                dout[row] = x[i];
+                // A's diagonal d; B's, where a = 0 and x is c times the square's
+                dout[row] = EPI == kMmGram ? x[i] : di * (args.cb + args.cc * di) + x[i];
                 x[i] = 0.0f;
               }
           }
@@ -513,13 +652,24 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           for (int i = 0; i < 4; ++i) v[i] = pack_half8(x + i * 8);
           __half* out = omat + static_cast<int64_t>(row) * args.ld + col;
           store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
-                        static_cast<int>(args.ld - col) / 8, lane, PutPlain{});
-          if (SYM && ti.m_blk != ti.n_blk && live) {
-            // the mirrored tile: consecutive lanes hold consecutive columns
-            __half* mir = omat + static_cast<int64_t>(col) * args.ld + row;
+                        (ld_end - col) / 8, lane, PutPlain{});
+          if (SYM && ti.m_blk != ti.n_blk) {
+            // the mirrored tile, transposed through the staging area: lane r
+            // writes column r, and its rows go out in 16-byte pieces
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (col + i < args.n) mir[static_cast<int64_t>(i) * args.ld] = __float2half_rn(x[i]);
+              reinterpret_cast<__half*>(stage + i * kStagePitch)[lane] = __float2half_rn(x[i]);
+            __syncwarp();
+            const int mrow0 = row - lane;  // the mirrored rows' first column
+#pragma unroll
+            for (int it4 = 0; it4 < 4; ++it4) {
+              const int j = it4 * 8 + lane / 4, piece = lane % 4;
+              const uint4 v4 = *reinterpret_cast<const uint4*>(stage + j * kStagePitch + piece * 16);
+              if (col + j < col_end && mrow0 + piece * 8 < args.ld)
+                *reinterpret_cast<uint4*>(omat + static_cast<int64_t>(col + j) * args.ld + mrow0 +
+                                          piece * 8) = v4;
+            }
+            __syncwarp();
           }
         }
       } else {
@@ -527,30 +677,30 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const float* diag = args.diag + static_cast<int64_t>(ti.g) * args.diag_ld;
         const int64_t src_stride = static_cast<int64_t>(args.m) * args.ld;
         const float drow = !args.diag_cols && live ? diag[row] : 0.0f;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int col = col0 + c * 32;
-          if (col >= args.n) break;
+          take_src(c);
+          if (col >= col_end) continue;
           float x[32];
           tmem_ld32(taddr + c * 32, x);
           tmem_ld_wait_regs(x);
           const int64_t at = ti.g * src_stride + static_cast<int64_t>(row) * args.ld + col;
-          const __half* hi = static_cast<const __half*>(args.src) + at;
-          const __half* lo = static_cast<const __half*>(args.src_lo) + at;
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
-            if (live && col + i < args.ld) {
-              float h[8], l[8];
-              unpack_half8(*reinterpret_cast<const uint4*>(hi + i), h);
-              unpack_half8(*reinterpret_cast<const uint4*>(lo + i), l);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float d =
-                    args.diag_cols ? (col + i + j < args.n ? diag[col + i + j] : 0.0f) : drow;
-                x[i + j] = args.ca * (h[j] + l[j]) + d * h[j] + x[i + j];
-              }
+            float h[8], l[8];
+            unpack_half8(*reinterpret_cast<const uint4*>(stage + lane * kStagePitch + i * 2), h);
+            unpack_half8(*reinterpret_cast<const uint4*>(stage + lane * kStagePitch + 64 + i * 2), l);
+            float d[8] = {drow, drow, drow, drow, drow, drow, drow, drow};
+            if (args.diag_cols && col + i < args.ld) {
+              Vec16<float>::load(diag + col + i, d);
+              Vec16<float>::load(diag + col + i + 4, d + 4);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              x[i + j] = args.ca * (h[j] + l[j]) + d[j] * h[j] + x[i + j];
           }
+          __syncwarp();
           if (args.out_lo != nullptr) {
             float l[32];
             uint4 v[4];
@@ -563,7 +713,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
               for (int j = 0; j < 8; ++j) l[i * 8 + j] = x[i * 8 + j] - h[j];
             }
-            const int pieces = static_cast<int>(args.ld - col) / 8;
+            const int pieces = (ld_end - col) / 8;
             __half* o = static_cast<__half*>(args.out) + at;
             store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(o) : nullptr, pieces, lane,
                           PutPlain{});
@@ -585,11 +735,11 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
               for (int i = 0; i < 4; ++i)
                 Vec16<bf16>::store(reinterpret_cast<bf16*>(&v[i]), x + i * 8);
               store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
-                            (args.n - col) / 8, lane, PutPlain{});
+                            (col_end - col) / 8, lane, PutPlain{});
             } else if (live) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (col + i < args.n) out[i] = __float2bfloat16_rn(x[i]);
+                if (col + i < col_end) out[i] = __float2bfloat16_rn(x[i]);
             }
           }
         }
@@ -625,13 +775,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-template <int LAYOUT, int SCHED, int EPI, bool FP16>
+template <int LAYOUT, int SCHED, int EPI, bool FP16, int AR = 128>
 int launch_impl(const CUtensorMap& a, const CUtensorMap& b, const MmArgs& args, int pairs,
                 cudaStream_t st) {
   static std::atomic<uint64_t> optin{0};
-  auto kern = mm_pair_kernel<LAYOUT, SCHED, EPI, FP16>;
-  if (int rc = ensure_smem_optin(reinterpret_cast<const void*>(kern), kSmemBytes, optin)) return rc;
-  return launch_k(kern, dim3(2 * pairs), kThreads, kSmemBytes, st, 2, a, b, args);
+  auto kern = mm_pair_kernel<LAYOUT, SCHED, EPI, FP16, AR>;
+  constexpr int smem = Stage<AR>::kSmem;
+  if (int rc = ensure_smem_optin(reinterpret_cast<const void*>(kern), smem, optin)) return rc;
+  return launch_k(kern, dim3(2 * pairs), kThreads, smem, st, 2, a, b, args);
+}
+
+template <int LAYOUT>
+int launch_rows(int rows, const CUtensorMap& a, const CUtensorMap& b, const MmArgs& args, int pairs,
+                cudaStream_t st) {
+  if (rows == kMmRows64)
+    return launch_impl<LAYOUT, kMmRaggedM, kMmStoreBf16, false, 64>(a, b, args, pairs, st);
+  return launch_impl<LAYOUT, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
 }
 
 }  // namespace
@@ -650,12 +809,12 @@ bool make_map_16bit(CUtensorMap* map, bool fp16, const void* base, uint64_t inne
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launch_mm(int layout, int sched, int epi, const CUtensorMap& a, const CUtensorMap& b,
+int launch_mm(int layout, int sched, int epi, int rows, const CUtensorMap& a, const CUtensorMap& b,
               const MmArgs& args, int pairs, cudaStream_t st) {
   if (pairs <= 0) return MOE_OK;
   if (sched == kMmRaggedM && epi == kMmStoreBf16) {
-    if (layout == kMmNT) return launch_impl<kMmNT, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
-    if (layout == kMmNN) return launch_impl<kMmNN, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
+    if (layout == kMmNT) return launch_rows<kMmNT>(rows, a, b, args, pairs, st);
+    if (layout == kMmNN) return launch_rows<kMmNN>(rows, a, b, args, pairs, st);
   }
   if (sched == kMmRaggedK && layout == kMmTN) {
     if (epi == kMmStoreBf16) return launch_impl<kMmTN, kMmRaggedK, kMmStoreBf16, false>(a, b, args, pairs, st);

@@ -43,6 +43,7 @@ struct MmArgs {
   int32_t groups;
   int32_t m;               // rows of D of one group (not kMmRaggedM)
   int32_t n;               // columns of D
+  int32_t tn;              // columns of a tile (mm_tile_width)
   int32_t k;               // reduction length (not kMmRaggedK)
   void* out;
   int64_t ld;              // elements between rows of out
@@ -66,12 +67,27 @@ struct MmArgs {
 bool make_map_16bit(CUtensorMap* map, bool fp16, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t depth, uint64_t ld, uint64_t stride, uint32_t box_rows);
 
-// Box rows of the A (or B) map of a layout: 128 rows K-major, 64 MN-major.
-inline uint32_t mm_box_a(int layout) { return layout == kMmTN ? 64u : 128u; }
+// Rows of A in a stage.  Where no group has more than 64 rows (decode), the
+// smaller box leaves room for seven stages of weights instead of five.
+enum MmRows { kMmRows128 = 128, kMmRows64 = 64 };
+
+// Columns of each of the equal tiles that n columns are cut into, at most 256,
+// in the MMA's steps of 32 (n = 1288: six tiles of 224, not five of 256 and
+// one of 8).
+inline int32_t mm_tile_width(int32_t n) {
+  const int32_t tiles = (n + 255) / 256;
+  return ((n + tiles - 1) / tiles + 31) / 32 * 32;
+}
+
+// Box rows of the A (or B) map of a layout: MN-major operands come in slices
+// of 64 k rows.
+inline uint32_t mm_box_a(int layout, int rows = kMmRows128) {
+  return layout == kMmTN ? 64u : static_cast<uint32_t>(rows);
+}
 inline uint32_t mm_box_b(int layout) { return layout == kMmNT ? 128u : 64u; }
 
 // `pairs` CTA pairs compute the product.
-int launch_mm(int layout, int sched, int epi, const CUtensorMap& a, const CUtensorMap& b,
+int launch_mm(int layout, int sched, int epi, int rows, const CUtensorMap& a, const CUtensorMap& b,
               const MmArgs& args, int pairs, cudaStream_t st);
 
 }  // namespace sm100

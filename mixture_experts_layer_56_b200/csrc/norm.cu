@@ -43,10 +43,23 @@ struct RowSlice {
   template <typename S>
   __device__ __forceinline__ static void load_f32(const S* p, int d, int t, int tpr, float fill,
                                                   float* v) {
+    if (VEC && sizeof(S) == 4) {
+      // a piece is 4 or 8 neighbours: whole 16-byte loads
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = col(i, t, tpr);
-      v[i] = c < d ? to_f32(p[c]) : fill;
+      for (int i = 0; i < V; i += 4) {
+        const int c = col(i, t, tpr);
+        if (c < d) {
+          Vec16<float>::load(reinterpret_cast<const float*>(p) + c, v + i);
+        } else {
+          v[i] = v[i + 1] = v[i + 2] = v[i + 3] = fill;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = col(i, t, tpr);
+        v[i] = c < d ? to_f32(p[c]) : fill;
+      }
     }
   }
   __device__ __forceinline__ static void load(const T* p, int d, int t, int tpr, float* v) {
@@ -103,52 +116,146 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
 
 template <int TPR> constexpr int block_of() { return TPR > 256 ? TPR : 256; }
 
-template <typename T, bool VEC, int TPR>
-__global__ void __launch_bounds__(block_of<TPR>())
-norm_fwd_kernel(const T* x, const float* __restrict__ gamma,
-                const float* __restrict__ beta, int64_t rows, int d, float eps,
-                T* y, float* __restrict__ mean, float* __restrict__ rstd) {
+// Rows on their way from memory: kRing rows per group, of each of the ARRAYS
+// that a pass reads, in shared memory, fetched with cp.async.  A thread copies exactly the values that it
+// will use, so that its own wait_group is all the waiting there is.
+constexpr int kRing = 3;
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T, bool VEC, int TPR, int ARRAYS>
+struct RowRing {
   using S = RowSlice<T, VEC>;
+  static constexpr int B = block_of<TPR>();
+  // odd widths of 2-byte values have no 4-byte alignment: loaded directly
+  static constexpr bool kAsync = VEC || sizeof(T) == 4;
+  static constexpr int kBytes = kAsync ? kRing * ARRAYS * S::V * B * static_cast<int>(sizeof(T)) : 0;
+
+  __device__ __forceinline__ static T* slot(uint8_t* base, int stage, int which, int i) {
+    // 16-byte pieces (VEC) or single values of all threads side by side
+    constexpr int N = VEC ? S::N : 1;
+    return reinterpret_cast<T*>(base) +
+           (static_cast<size_t>((stage * ARRAYS + which) * (S::V / N) + i) * B + threadIdx.x) * N;
+  }
+  __device__ __forceinline__ static void fetch(uint8_t* base, int stage, int which, const T* p,
+                                               int d, int t) {
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < S::P; ++i) {
+        const int c = (t + i * TPR) * S::N;
+        if (c < d) copy_async16(slot(base, stage, which, i), p + c);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::V; ++i) {
+        const int c = t + i * TPR;
+        if (c < d) copy_async4(slot(base, stage, which, i), p + c);
+      }
+    }
+  }
+  __device__ __forceinline__ static void take(uint8_t* base, int stage, int which, int d, int t,
+                                              float* v) {
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < S::P; ++i) {
+        if ((t + i * TPR) * S::N < d) {
+          Vec16<T>::load(slot(base, stage, which, i), v + i * S::N);
+        } else {
+#pragma unroll
+          for (int j = 0; j < S::N; ++j) v[i * S::N + j] = 0.0f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::V; ++i)
+        v[i] = t + i * TPR < d ? to_f32(*slot(base, stage, which, i)) : 0.0f;
+    }
+  }
+};
+
+template <typename T, bool VEC, int TPR>
+__global__ void __launch_bounds__(block_of<TPR>(), TPR > 256 ? 1 : 3)
+norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __restrict__ beta,
+                int64_t rows, int d, float eps, T* y, float* __restrict__ mean,
+                float* __restrict__ rstd) {
+  using S = RowSlice<T, VEC>;
+  using R = RowRing<T, VEC, TPR, 1>;
   constexpr int V = S::V;
   constexpr int RG = block_of<TPR>() / TPR;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][block_of<TPR>() / 32];
   pdl_wait();
   pdl_trigger();
   const int t = threadIdx.x % TPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * RG + threadIdx.x / TPR;
-  const bool live = row < rows;
-  float v[V];
-  if (live) {
-    S::load(x + row * d, d, t, TPR, v);
+  const int grp = threadIdx.x / TPR;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * RG;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * RG + grp;
+  auto fetch = [&](int64_t row, int stage) {
+    if (R::kAsync && row < rows) R::fetch(ring, stage, 0, x + row * d, d, t);
+    if (R::kAsync) copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kRing - 1; ++s) fetch(first + s * step, s);
+  float g[V], b[V];
+  S::load_f32(gamma, d, t, TPR, 0.0f, g);
+  if (beta != nullptr) {
+    S::load_f32(beta, d, t, TPR, 0.0f, b);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    for (int i = 0; i < V; ++i) b[i] = 0.0f;
   }
-  float s = 0.0f;
+  int stage = 0;
+  // every group of the block takes the same number of turns
+  for (int64_t row = first; row - grp < rows; row += step) {
+    const bool live = row < rows;
+    fetch(row + (kRing - 1) * step, (stage + kRing - 1) % kRing);
+    float v[V];
+    if (live) {
+      if (R::kAsync) {
+        copy_wait<kRing - 1>();
+        R::take(ring, stage, 0, d, t, v);
+      } else {
+        S::load(x + row * d, d, t, TPR, v);
+      }
+    } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) s += v[i];
-  const float mu = group_sum<TPR>(s, red[0]) / d;
-  float q = 0.0f;
+      for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    }
+    stage = (stage + 1) % kRing;
+    float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    v[i] = S::col(i, t, TPR) < d ? v[i] - mu : 0.0f;
-    q += v[i] * v[i];
-  }
-  const float rs = 1.0f / sqrtf(group_sum<TPR>(q, red[1]) / d + eps);
-  if (!live) return;
-  float g[V];
-  S::load_f32(gamma, d, t, TPR, 0.0f, g);
+    for (int i = 0; i < V; ++i) s += v[i];
+    const float mu = group_sum<TPR>(s, red[0]) / d;
+    float q = 0.0f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = v[i] * rs * g[i];
-  if (beta != nullptr) {
-    S::load_f32(beta, d, t, TPR, 0.0f, g);
+    for (int i = 0; i < V; ++i) {
+      v[i] = S::col(i, t, TPR) < d ? v[i] - mu : 0.0f;
+      q += v[i] * v[i];
+    }
+    const float rs = 1.0f / sqrtf(group_sum<TPR>(q, red[1]) / d + eps);
+    if (!live) continue;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += g[i];
-  }
-  S::store(y + row * d, d, t, TPR, v);
-  if (t == 0) {
-    if (mean != nullptr) mean[row] = mu;
-    if (rstd != nullptr) rstd[row] = rs;
+    for (int i = 0; i < V; ++i) v[i] = v[i] * rs * g[i] + b[i];
+    S::store(y + row * d, d, t, TPR, v);
+    if (t == 0) {
+      if (mean != nullptr) mean[row] = mu;
+      if (rstd != nullptr) rstd[row] = rs;
+    }
   }
 }
 
@@ -183,47 +290,79 @@ norm_fwd_wide_kernel(const T* x, const float* __restrict__ gamma,
 }
 
 template <typename T, bool VEC, int TPR>
+constexpr int bwd_smem() {
+  constexpr int ring = RowRing<T, VEC, TPR, 2>::kBytes;
+  constexpr int sums = block_of<TPR>() > TPR ? block_of<TPR>() * NormCfg<T>::kVals * 4 : 0;
+  return ring > sums ? ring : sums;
+}
+
+template <typename T, bool VEC, int TPR>
 __global__ void __launch_bounds__(block_of<TPR>(), TPR > 256 ? 1 : 2)
 norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ gamma,
                 const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows,
                 int d, T* dx, float* __restrict__ part) {
   using S = RowSlice<T, VEC>;
+  using R = RowRing<T, VEC, TPR, 2>;
   constexpr int V = S::V;
   constexpr int B = block_of<TPR>();
   constexpr int RG = B / TPR;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][2][B / 32];
-  __shared__ float acc[RG > 1 ? B * V : 1];
   pdl_wait();
   pdl_trigger();
   const int t = threadIdx.x % TPR;
   const int grp = threadIdx.x / TPR;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * RG;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * RG + grp;
+  auto fetch = [&](int64_t row, int stage) {
+    if (R::kAsync && row < rows) {
+      R::fetch(ring, stage, 0, x + row * d, d, t);
+      R::fetch(ring, stage, 1, dy + row * d, d, t);
+    }
+    if (R::kAsync) copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kRing - 1; ++s) fetch(first + s * step, s);
   float g[V], dg[V], db[V];
   S::load_f32(gamma, d, t, TPR, 0.0f, g);
 #pragma unroll
   for (int i = 0; i < V; ++i) dg[i] = db[i] = 0.0f;
   const float inv_d = 1.0f / d;
-  int buf = 0;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * RG; base < rows;
-       base += static_cast<int64_t>(gridDim.x) * RG, buf ^= 1) {
-    const int64_t row = base + grp;
+  float mu = 0.0f, rs = 0.0f;
+  if (first < rows) {
+    mu = mean[first];
+    rs = rstd[first];
+  }
+  int buf = 0, stage = 0;
+  // every group of the block takes the same number of turns
+  for (int64_t row = first; row - grp < rows; row += step, buf ^= 1) {
     const bool live = row < rows;
+    fetch(row + (kRing - 1) * step, (stage + kRing - 1) % kRing);
+    float mu_next = 0.0f, rs_next = 0.0f;
+    if (row + step < rows) {
+      mu_next = mean[row + step];
+      rs_next = rstd[row + step];
+    }
     float h[V], v[V];
-    float rs = 0.0f;
     if (live) {
-      S::load(x + row * d, d, t, TPR, h);
-      S::load(dy + row * d, d, t, TPR, v);
-      const float mu = mean[row];
-      rs = rstd[row];
-#pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = (h[i] - mu) * rs;
+      if (R::kAsync) {
+        copy_wait<kRing - 1>();
+        R::take(ring, stage, 0, d, t, h);
+        R::take(ring, stage, 1, d, t, v);
+      } else {
+        S::load(x + row * d, d, t, TPR, h);
+        S::load(dy + row * d, d, t, TPR, v);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) h[i] = v[i] = 0.0f;
     }
+    stage = (stage + 1) % kRing;
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       // past the row dy and gamma are 0, and h is not used
+      h[i] = (h[i] - mu) * rs;
       dg[i] += v[i] * h[i];
       db[i] += v[i];
       v[i] *= g[i];
@@ -260,6 +399,8 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
       for (int i = 0; i < V; ++i) v[i] = rs * (v[i] - s1 - h[i] * s2);
       S::store(dx + row * d, d, t, TPR, v);
     }
+    mu = mu_next;
+    rs = rs_next;
   }
   // this block's sums: part[0] dgamma, part[1] dbeta, [gridDim.x, d] each
   float* pg = part + static_cast<int64_t>(blockIdx.x) * d;
@@ -274,6 +415,8 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
       }
     }
   } else {
+    // the copies of rows past the last were never issued: the ring is free
+    float* acc = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
       __syncthreads();
@@ -383,21 +526,26 @@ int part_rows_of(int64_t T_, int d, int sms) {
 
 template <typename T, bool VEC, int TPR>
 int fwd_impl(const T* x, const float* gamma, const float* beta, int64_t rows, int d, float eps,
-             T* y, float* mean, float* rstd, cudaStream_t st) {
+             T* y, float* mean, float* rstd, int sms, cudaStream_t st) {
   constexpr int RG = block_of<TPR>() / TPR;
-  return launch_k(norm_fwd_kernel<T, VEC, TPR>, dim3(static_cast<unsigned>((rows + RG - 1) / RG)),
-                  dim3(block_of<TPR>()), 0, st, 1, x, gamma, beta, rows, d, eps, y, mean, rstd);
+  constexpr int smem = RowRing<T, VEC, TPR, 1>::kBytes;
+  static std::atomic<uint64_t> optin{0};
+  auto kern = norm_fwd_kernel<T, VEC, TPR>;
+  if (int rc = ensure_smem_optin(reinterpret_cast<const void*>(kern), smem, optin)) return rc;
+  const int64_t blocks = (rows + RG - 1) / RG, most = static_cast<int64_t>(sms) * (TPR > 256 ? 2 : 3);
+  return launch_k(kern, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                  dim3(block_of<TPR>()), smem, st, 1, x, gamma, beta, rows, d, eps, y, mean, rstd);
 }
 
 template <typename T, bool VEC>
 int fwd_group(const T* x, const float* gamma, const float* beta, int64_t rows, int d, float eps,
-              T* y, float* mean, float* rstd, cudaStream_t st) {
+              T* y, float* mean, float* rstd, int sms, cudaStream_t st) {
   switch (group_of<T>(d)) {
-    case 32: return fwd_impl<T, VEC, 32>(x, gamma, beta, rows, d, eps, y, mean, rstd, st);
-    case 64: return fwd_impl<T, VEC, 64>(x, gamma, beta, rows, d, eps, y, mean, rstd, st);
-    case 128: return fwd_impl<T, VEC, 128>(x, gamma, beta, rows, d, eps, y, mean, rstd, st);
-    case 256: return fwd_impl<T, VEC, 256>(x, gamma, beta, rows, d, eps, y, mean, rstd, st);
-    case 512: return fwd_impl<T, VEC, 512>(x, gamma, beta, rows, d, eps, y, mean, rstd, st);
+    case 32: return fwd_impl<T, VEC, 32>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
+    case 64: return fwd_impl<T, VEC, 64>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
+    case 128: return fwd_impl<T, VEC, 128>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
+    case 256: return fwd_impl<T, VEC, 256>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
+    case 512: return fwd_impl<T, VEC, 512>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
   }
   return launch_k(norm_fwd_wide_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, 1,
                   x, gamma, beta, d, eps, y, mean, rstd);
@@ -405,18 +553,21 @@ int fwd_group(const T* x, const float* gamma, const float* beta, int64_t rows, i
 
 template <typename T>
 int fwd_typed(const void* x, const float* gamma, const float* beta, int64_t rows, int d, float eps,
-              void* y, float* mean, float* rstd, cudaStream_t st) {
+              void* y, float* mean, float* rstd, int sms, cudaStream_t st) {
   const T* xt = static_cast<const T*>(x);
   T* yt = static_cast<T*>(y);
-  return d % Vec16<T>::N == 0 ? fwd_group<T, true>(xt, gamma, beta, rows, d, eps, yt, mean, rstd, st)
-                              : fwd_group<T, false>(xt, gamma, beta, rows, d, eps, yt, mean, rstd, st);
+  return d % Vec16<T>::N == 0 ? fwd_group<T, true>(xt, gamma, beta, rows, d, eps, yt, mean, rstd, sms, st)
+                              : fwd_group<T, false>(xt, gamma, beta, rows, d, eps, yt, mean, rstd, sms, st);
 }
 
 template <typename T, bool VEC, int TPR>
 int bwd_impl(const T* dy, const T* x, const float* gamma, const float* mean, const float* rstd,
              int64_t rows, int d, T* dx, float* part, int part_rows, cudaStream_t st) {
-  return launch_k(norm_bwd_kernel<T, VEC, TPR>, dim3(part_rows), dim3(block_of<TPR>()), 0, st, 1,
-                  dy, x, gamma, mean, rstd, rows, d, dx, part);
+  static std::atomic<uint64_t> optin{0};
+  auto kern = norm_bwd_kernel<T, VEC, TPR>;
+  constexpr int smem = bwd_smem<T, VEC, TPR>();
+  if (int rc = ensure_smem_optin(reinterpret_cast<const void*>(kern), smem, optin)) return rc;
+  return launch_k(kern, dim3(part_rows), dim3(block_of<TPR>()), smem, st, 1, dy, x, gamma, mean, rstd, rows, d, dx, part);
 }
 
 template <typename T, bool VEC>
@@ -451,10 +602,11 @@ int bwd_typed(const void* dy, const void* x, const float* gamma, const float* me
 }  // namespace
 
 int launch_layer_norm(int dtype, const void* x, const float* gamma, const float* beta, int64_t T,
-                      int d, float eps, void* y, float* mean, float* rstd, cudaStream_t st) {
+                      int d, float eps, void* y, float* mean, float* rstd, int sms,
+                      cudaStream_t st) {
   return dtype == MOE_DTYPE_BF16
-             ? fwd_typed<bf16>(x, gamma, beta, T, d, eps, y, mean, rstd, st)
-             : fwd_typed<float>(x, gamma, beta, T, d, eps, y, mean, rstd, st);
+             ? fwd_typed<bf16>(x, gamma, beta, T, d, eps, y, mean, rstd, sms, st)
+             : fwd_typed<float>(x, gamma, beta, T, d, eps, y, mean, rstd, sms, st);
 }
 
 int norm_partial_rows(int dtype, int64_t T, int d, int sms) {

@@ -220,12 +220,13 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
     a.diag_ld = static_cast<int32_t>(L.ldm);
     // A = X X^T
     a.m = a.n = L.m;
+    a.tn = 256;  // square tiles: the symmetric products skip those above the diagonal
     a.k = tall ? rows : cols;
     a.out = ws + L.gram;
     a.ld = L.ldm;
     a.out_stride = static_cast<int64_t>(gs);
     a.diag_out = reinterpret_cast<float*>(ws + L.dgram);
-    if (int e = launch_mm(gram_layout, kMmBatchSym, kMmGram, xg[cur], xg[cur], a, sym_pairs, st))
+    if (int e = launch_mm(gram_layout, kMmBatchSym, kMmGram, kMmRows128, xg[cur], xg[cur], a, sym_pairs, st))
       return e;
     // B = b A + c A A
     a.k = L.m;
@@ -233,11 +234,12 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
     a.diag = reinterpret_cast<const float*>(ws + L.dgram);
     a.out = ws + L.poly;
     a.diag_out = reinterpret_cast<float*>(ws + L.dpoly);
-    if (int e = launch_mm(kMmNT, kMmBatchSym, kMmPoly, ga, ga, a, sym_pairs, st)) return e;
+    if (int e = launch_mm(kMmNT, kMmBatchSym, kMmPoly, kMmRows128, ga, ga, a, sym_pairs, st)) return e;
     // X <- a X + B X, the last time as bf16 into O
     const bool last = s == steps - 1;
     a.m = rows;
     a.n = cols;
+    a.tn = mm_tile_width(cols);
     a.src = ws + (cur ? L.hi1 : L.hi0);
     a.src_lo = ws + L.lo;
     a.diag = reinterpret_cast<const float*>(ws + L.dpoly);
@@ -253,7 +255,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
       a.out_stride = static_cast<int64_t>(xs);
       a.out_lo = ws + L.lo;  // each element is read and then written by one thread
     }
-    if (int e = launch_mm(upd_layout, kMmBatch, kMmUpdate, tall ? xu[cur] : ba, tall ? ba : xu[cur],
+    if (int e = launch_mm(upd_layout, kMmBatch, kMmUpdate, kMmRows128, tall ? xu[cur] : ba, tall ? ba : xu[cur],
                           a, upd_pairs, st))
       return e;
   }

@@ -17,7 +17,6 @@ template <typename... P> bool any_null(P... p) { return ((p == nullptr) || ...);
 template <typename... P> bool any_misaligned(P... p) { return (misaligned(p) || ...); }
 
 inline bool known_dtype(int32_t t) { return t == MOE_DTYPE_F32 || t == MOE_DTYPE_BF16; }
-inline int64_t elem_bytes(int32_t t) { return t == MOE_DTYPE_BF16 ? 2 : 4; }
 
 constexpr size_t kStatusBytes = 256;  // the status word at the workspace's start
 constexpr int32_t kMaxSide = 1 << 24;
@@ -89,8 +88,9 @@ int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const
   const int layout = dx ? kMmNN : kMmNT;
   const int32_t n = dx ? s.k : s.n, k = dx ? s.n : s.k;  // of the product
   const uint64_t k64 = k, rows = s.rows, wn = s.n, wk = s.k;
+  const int box = s.rows <= 64 ? kMmRows64 : kMmRows128;
   CUtensorMap ma, mb;
-  if (!make_map_16bit(&ma, false, in, k64, rows, 1, k64, rows * k64, mm_box_a(layout)) ||
+  if (!make_map_16bit(&ma, false, in, k64, rows, 1, k64, rows * k64, mm_box_a(layout, box)) ||
       !make_map_16bit(&mb, false, W, wk, wn, s.n_groups, wk, wn * wk, mm_box_b(layout)))
     return MOE_ERR_CUDA;
   MmArgs a{};
@@ -102,8 +102,9 @@ int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const
   a.out = out;
   a.ld = n;
   a.status = static_cast<int32_t*>(ws);
-  return launch_mm(layout, kMmRaggedM, kMmStoreBf16, ma, mb, a,
-                   pairs_for(ragged_row_blocks(s) * ((n + 255) / 256), sms), st);
+  a.tn = mm_tile_width(n);
+  return launch_mm(layout, kMmRaggedM, kMmStoreBf16, box, ma, mb, a,
+                   pairs_for(ragged_row_blocks(s) * ((n + a.tn - 1) / a.tn), sms), st);
 }
 
 int check_grouped(const moe_grouped_shape_t& s, const void* in, const int32_t* offsets,
@@ -200,13 +201,14 @@ int moe_grouped_matmul_dw(const moe_grouped_shape_t* shape, const void* dY, cons
   a.groups = s.n_groups;
   a.m = s.n;
   a.n = s.k;
+  a.tn = mm_tile_width(s.k);
   a.out = dW;
   a.ld = s.k;
   a.out_stride = static_cast<int64_t>(s.n) * s.k;
   a.status = static_cast<int32_t*>(ws);
   const int epi = add ? kMmAddF32 : (f32_out ? kMmStoreF32 : kMmStoreBf16);
-  const int64_t tiles = static_cast<int64_t>(s.n_groups) * ((s.n + 255) / 256) * ((s.k + 255) / 256);
-  return launch_mm(kMmTN, kMmRaggedK, epi, ma, mb, a, pairs_for(tiles, sms), st);
+  const int64_t tiles = static_cast<int64_t>(s.n_groups) * ((s.n + 255) / 256) * ((s.k + a.tn - 1) / a.tn);
+  return launch_mm(kMmTN, kMmRaggedK, epi, kMmRows128, ma, mb, a, pairs_for(tiles, sms), st);
 }
 
 int moe_swiglu(const moe_swiglu_shape_t* shape, const void* gu, void* a, moe_stream_t stream) {
@@ -247,7 +249,7 @@ int moe_layer_norm(const moe_norm_shape_t* shape, const void* x, const float* ga
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   StageScope sg(MOE_KERNEL_LAYER_NORM, st);
   return launch_layer_norm(shape->dtype, x, gamma, beta, shape->T, shape->d, shape->eps, y, mean,
-                           rstd, st);
+                           rstd, sms, st);
 }
 
 int moe_layer_norm_workspace_size(const moe_norm_shape_t* shape, size_t* bytes) {

@@ -17,7 +17,8 @@ int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* o
 
 // layer norm (norm.cu)
 int launch_layer_norm(int dtype, const void* x, const float* gamma, const float* beta, int64_t T,
-                      int d, float eps, void* y, float* mean, float* rstd, cudaStream_t st);
+                      int d, float eps, void* y, float* mean, float* rstd, int sms,
+                      cudaStream_t st);
 // SMs that a backward pass's workspace is sized for, so that its size needs no
 // device (148 on a B200)
 constexpr int kNormMaxSms = 160;

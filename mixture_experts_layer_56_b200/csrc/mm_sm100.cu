@@ -86,10 +86,9 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint4* v, uint8
   __syncwarp();
 }
 
-// The other way round: a warp's 32 rows of 64 bytes (32 fp16 values), read as
-// whole row segments.  fetch() starts the loads (rows at or past `rows` and
-// pieces past the matrix give zeros), put() leaves row r's bytes at
-// stage + r * kStagePitch + offset for lane r.
+// A warp's 32 rows of 32 fp16 values as whole row segments: piece `it` of a
+// lane is row it * 8 + lane / 4, columns 8 (lane % 4) .. + 7.  Rows at or past
+// `rows` and pieces past the matrix give zeros.
 struct RowFetch {
   uint4 v[4];
   __device__ __forceinline__ void fetch(const __half* base, int64_t ld, int rows, int pieces,
@@ -101,12 +100,6 @@ struct RowFetch {
                   ? *reinterpret_cast<const uint4*>(base + row * ld + c * 8)
                   : make_uint4(0, 0, 0, 0);
     }
-  }
-  __device__ __forceinline__ void put(uint8_t* stage, int offset, int lane) const {
-#pragma unroll
-    for (int it = 0; it < 4; ++it)
-      *reinterpret_cast<uint4*>(stage + (it * 8 + lane / 4) * kStagePitch + offset +
-                                (lane % 4) * 16) = v[it];
   }
 };
 
@@ -533,13 +526,30 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const Tile ti = SRC ? following : tile_of(tile);
       const bool more = tile + nclusters < total_tiles;
       if (SRC && more) following = tile_of(tile + nclusters);
-      // puts chunk c of src into the staging area and fetches the one after next
-      auto take_src = [&](int c) {
-        src_hi[c & 1].put(stage, 0, lane);
-        if (EPI == kMmUpdate) src_lo[c & 1].put(stage, 64, lane);
-        __syncwarp();
+      auto fetch_ahead = [&](int c) {
         if (c < 2) fetch_src(ti, c + 2);
         else if (more) fetch_src(following, c - 2);
+      };
+      // 32 accumulator columns through the staging area, from a row per lane to
+      // RowFetch's pieces: the one crossing that this epilogue makes, since
+      // shared memory also feeds the MMAs and is what they contend for (src
+      // and results crossing instead cost 5 x 0.2 ms more at 64 x 2048 x 1408)
+      auto stage_acc = [&](uint32_t addr) {
+        float x[32];
+        tmem_ld32(addr, x);
+        tmem_ld_wait_regs(x);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(stage + lane * kStagePitch + i * 16) =
+              make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        __syncwarp();
+      };
+      auto take_acc = [&](int it4, float* y) {
+        const float* p = reinterpret_cast<const float*>(
+            stage + (it4 * 8 + lane / 4) * kStagePitch + (lane % 4) * 32);
+        Vec16<float>::load(p, y);
+        Vec16<float>::load(p + 4, y + 4);
       };
       const bool empty = RAG_K && ti.nkb == 0;
       const int acc = it & 1;
@@ -604,46 +614,24 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
               store_rows<8>(stage, v, dst, (col_end - col) / 4, lane, PutPlain{});
           }
         }
-      } else if (EPI == kMmGram || EPI == kMmPoly) {
+      } else if (EPI == kMmGram) {
         // fp16 off the diagonal, the diagonal itself in fp32 apart
-        const float* diag = EPI == kMmPoly ? args.diag + static_cast<int64_t>(ti.g) * args.diag_ld
-                                           : nullptr;
         float* dout = args.diag_out + static_cast<int64_t>(ti.g) * args.diag_ld;
         __half* omat = static_cast<__half*>(args.out) + ti.g * args.out_stride;
-        const float di = EPI == kMmPoly && live ? diag[row] : 0.0f;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           const int col = col0 + c * 32;
-          if (SRC) take_src(c);
-          if (col >= col_end) continue;
+          if (col >= col_end) break;
           float x[32];
           tmem_ld32(taddr + c * 32, x);
           tmem_ld_wait_regs(x);
-          if (EPI == kMmGram) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] *= args.inv_scale2;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              float a[8];
-              unpack_half8(*reinterpret_cast<const uint4*>(stage + lane * kStagePitch + i * 2), a);
-              if (col + i < args.ld) {
-                const float4 d0 = *reinterpret_cast<const float4*>(diag + col + i);
-                const float4 d1 = *reinterpret_cast<const float4*>(diag + col + i + 4);
-                const float dj[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  x[i + j] = args.cb * a[j] + args.cc * ((di + dj[j]) * a[j] + x[i + j]);
-              }
-            }
-            __syncwarp();
-          }
+          for (int i = 0; i < 32; ++i) x[i] *= args.inv_scale2;
           if (live && row >= col && row < col + 32) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (col + i == row) {
-                // A's diagonal d; B's, where a = 0 and x is c times the square's
-                dout[row] = EPI == kMmGram ? x[i] : di * (args.cb + args.cc * di) + x[i];
+                dout[row] = x[i];
                 x[i] = 0.0f;
               }
           }
@@ -654,8 +642,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
                         (ld_end - col) / 8, lane, PutPlain{});
           if (SYM && ti.m_blk != ti.n_blk) {
-            // the mirrored tile, transposed through the staging area: lane r
-            // writes column r, and its rows go out in 16-byte pieces
+            // the mirrored tile: lane r writes column r of the staging area,
+            // whose rows go out in 16-byte pieces
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               reinterpret_cast<__half*>(stage + i * kStagePitch)[lane] = __float2half_rn(x[i]);
@@ -672,76 +660,138 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             __syncwarp();
           }
         }
-      } else {
-        // X' = a (hi + lo) + d hi + (B off its diagonal) hi, all times `scale`
+      } else if (EPI == kMmPoly) {
+        // off the diagonal b a + c ((d_i + d_j) a + o), o the product of A's
+        // off-diagonal parts; on it, where a = 0, b d + c (d^2 + o)
         const float* diag = args.diag + static_cast<int64_t>(ti.g) * args.diag_ld;
-        const int64_t src_stride = static_cast<int64_t>(args.m) * args.ld;
-        const float drow = !args.diag_cols && live ? diag[row] : 0.0f;
+        float* dout = args.diag_out + static_cast<int64_t>(ti.g) * args.diag_ld;
+        __half* omat = static_cast<__half*>(args.out) + ti.g * args.out_stride;
+        const int row0 = row - lane;
+        float di[4];
+#pragma unroll
+        for (int it4 = 0; it4 < 4; ++it4) {
+          const int pr = row0 + it4 * 8 + lane / 4;
+          di[it4] = pr < args.m ? diag[pr] : 0.0f;
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int col = col0 + c * 32;
-          take_src(c);
-          if (col >= col_end) continue;
-          float x[32];
-          tmem_ld32(taddr + c * 32, x);
-          tmem_ld_wait_regs(x);
-          const int64_t at = ti.g * src_stride + static_cast<int64_t>(row) * args.ld + col;
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float h[8], l[8];
-            unpack_half8(*reinterpret_cast<const uint4*>(stage + lane * kStagePitch + i * 2), h);
-            unpack_half8(*reinterpret_cast<const uint4*>(stage + lane * kStagePitch + 64 + i * 2), l);
-            float d[8] = {drow, drow, drow, drow, drow, drow, drow, drow};
-            if (args.diag_cols && col + i < args.ld) {
-              Vec16<float>::load(diag + col + i, d);
-              Vec16<float>::load(diag + col + i + 4, d + 4);
+          const int pc = col + (lane % 4) * 8;  // first column of this lane's pieces
+          uint4 out[4];
+          if (col < col_end) {
+            stage_acc(taddr + c * 32);
+            float dj[8] = {};
+            if (pc < args.ld) {
+              Vec16<float>::load(diag + pc, dj);
+              Vec16<float>::load(diag + pc + 4, dj + 4);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              x[i + j] = args.ca * (h[j] + l[j]) + d[j] * h[j] + x[i + j];
-          }
-          __syncwarp();
-          if (args.out_lo != nullptr) {
-            float l[32];
-            uint4 v[4];
+            for (int it4 = 0; it4 < 4; ++it4) {
+              const int pr = row0 + it4 * 8 + lane / 4;
+              float a[8], y[8];
+              unpack_half8(src_hi[c & 1].v[it4], a);
+              take_acc(it4, y);
+              const float d = di[it4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = pack_half8(x + i * 8);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float h[8];
-              unpack_half8(v[i], h);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) l[i * 8 + j] = x[i * 8 + j] - h[j];
-            }
-            const int pieces = (ld_end - col) / 8;
-            __half* o = static_cast<__half*>(args.out) + at;
-            store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(o) : nullptr, pieces, lane,
-                          PutPlain{});
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = pack_half8(l + i * 8);
-            o = static_cast<__half*>(args.out_lo) + at;
-            store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(o) : nullptr, pieces, lane,
-                          PutPlain{});
-          } else {
-            // the last step: bf16 in the caller's dense layout
-            const float inv = 1.0f / args.scale;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] *= inv;
-            bf16* out = static_cast<bf16*>(args.out) + ti.g * args.out_stride +
-                        static_cast<int64_t>(row) * args.n + col;
-            if (args.vec_ok) {
-              uint4 v[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                Vec16<bf16>::store(reinterpret_cast<bf16*>(&v[i]), x + i * 8);
-              store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
-                            (col_end - col) / 8, lane, PutPlain{});
-            } else if (live) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (col + i < col_end) out[i] = __float2bfloat16_rn(x[i]);
+              for (int j = 0; j < 8; ++j) {
+                y[j] = args.cb * a[j] + args.cc * ((d + dj[j]) * a[j] + y[j]);
+                if (pc + j == pr) {
+                  if (pr < args.m) dout[pr] = y[j] + d * (args.cb + args.cc * d);
+                  y[j] = 0.0f;
+                }
+              }
+              out[it4] = pack_half8(y);
+              if (pr < args.m && pc < ld_end)
+                *reinterpret_cast<uint4*>(omat + static_cast<int64_t>(pr) * args.ld + pc) = out[it4];
             }
           }
+          fetch_ahead(c);
+          if (col < col_end && ti.m_blk != ti.n_blk) {
+            // the mirrored tile, transposed through the staging area in rows of
+            // 72 bytes
+            constexpr int pitch = 72;
+            __syncwarp();
+#pragma unroll
+            for (int it4 = 0; it4 < 4; ++it4) {
+              const __half* h = reinterpret_cast<const __half*>(&out[it4]);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                reinterpret_cast<__half*>(stage + ((lane % 4) * 8 + j) * pitch)[it4 * 8 + lane / 4] =
+                    h[j];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int j = k * 4 + lane / 8, piece = lane % 8;
+              const uint2 v2 = *reinterpret_cast<const uint2*>(stage + j * pitch + piece * 8);
+              if (col + j < col_end && row0 + piece * 4 < args.ld)
+                *reinterpret_cast<uint2*>(omat + static_cast<int64_t>(col + j) * args.ld + row0 +
+                                          piece * 4) = v2;
+            }
+            __syncwarp();
+          }
+        }
+      } else {
+        // X' = a (hi + lo) + d hi + (B off its diagonal) hi, all times `scale`;
+        // d is B's diagonal, of the row where B stands on the left
+        const float* diag = args.diag + static_cast<int64_t>(ti.g) * args.diag_ld;
+        const int64_t src_base = ti.g * (static_cast<int64_t>(args.m) * args.ld);
+        const bool last = args.out_lo == nullptr;
+        const float inv = 1.0f / args.scale;
+        const int row0 = row - lane;
+        float dr[4];
+#pragma unroll
+        for (int it4 = 0; it4 < 4; ++it4) {
+          const int pr = row0 + it4 * 8 + lane / 4;
+          dr[it4] = !args.diag_cols && pr < args.m ? diag[pr] : 0.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = col0 + c * 32;
+          const int pc = col + (lane % 4) * 8;
+          if (col < col_end) {
+            stage_acc(taddr + c * 32);
+            float dc[8] = {};
+            if (args.diag_cols && pc < args.ld) {
+              Vec16<float>::load(diag + pc, dc);
+              Vec16<float>::load(diag + pc + 4, dc + 4);
+            }
+#pragma unroll
+            for (int it4 = 0; it4 < 4; ++it4) {
+              const int pr = row0 + it4 * 8 + lane / 4;
+              float h[8], l[8], y[8];
+              unpack_half8(src_hi[c & 1].v[it4], h);
+              unpack_half8(src_lo[c & 1].v[it4], l);
+              take_acc(it4, y);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                y[j] = args.ca * (h[j] + l[j]) + (dr[it4] + dc[j]) * h[j] + y[j];
+              if (pr >= args.m || pc >= ld_end) continue;
+              if (!last) {
+                const int64_t at = src_base + static_cast<int64_t>(pr) * args.ld + pc;
+                const uint4 hv = pack_half8(y);
+                *reinterpret_cast<uint4*>(static_cast<__half*>(args.out) + at) = hv;
+                unpack_half8(hv, h);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] -= h[j];
+                *reinterpret_cast<uint4*>(static_cast<__half*>(args.out_lo) + at) = pack_half8(y);
+              } else {
+                // the last step: bf16 in the caller's dense layout
+                bf16* out = static_cast<bf16*>(args.out) + ti.g * args.out_stride +
+                            static_cast<int64_t>(pr) * args.n + pc;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] *= inv;
+                if (args.vec_ok) {
+                  Vec16<bf16>::store(out, y);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    if (pc + j < col_end) out[j] = __float2bfloat16_rn(y[j]);
+                }
+              }
+            }
+          }
+          fetch_ahead(c);
         }
       }
       if (!empty) {

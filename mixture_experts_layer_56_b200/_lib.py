@@ -162,17 +162,29 @@ def strerror(code: int) -> str:
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
     return x.data_ptr()
 
 
+_current_raw_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_raw_stream
+        if _current_raw_stream is None:
+            import torch
+            raw, device = (getattr(torch._C, n, None)
+                           for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            if raw is not None and device is not None:
+                # current_stream() without its Stream object, which costs more
+                # than a small kernel takes to launch
+                torch.cuda.init()
+                _current_raw_stream = lambda: raw(device())  # noqa: E731
+            else:
+                _current_raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        return _current_raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

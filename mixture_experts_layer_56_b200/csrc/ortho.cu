@@ -162,6 +162,10 @@ OrthoLayout ortho_layout(int mats, int rows, int cols) {
     return at;
   };
   L.status = take(256);
+  if (ortho_small_fits(rows, cols)) {
+    L.total = o;
+    return L;
+  }
   L.partial = take(n * L.parts * 8);
   L.hi0 = take(x);
   L.hi1 = take(x);
@@ -182,6 +186,9 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
   const int longest = rows > cols ? rows : cols;
   float scale = 1.0f;
   while (scale * scale * 4.0f <= static_cast<float>(longest)) scale *= 2.0f;
+  if (ortho_small_fits(rows, cols))
+    return launch_ortho_small(dtype, M, O, mats, rows, cols, steps, coef, scale,
+                              reinterpret_cast<int32_t*>(ws + L.status), st);
   const int rc = dtype == MOE_DTYPE_BF16
                      ? launch_prepare<bf16>(M, mats, rows, cols, L, scale, ws, st)
                      : launch_prepare<float>(M, mats, rows, cols, L, scale, ws, st);

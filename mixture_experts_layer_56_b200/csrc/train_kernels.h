@@ -42,6 +42,10 @@ struct OrthoLayout {
   int m;              // min(rows, cols)
 };
 OrthoLayout ortho_layout(int mats, int rows, int cols);
+// small matrices: one kernel, no workspace but the status word (ortho_small.cu)
+bool ortho_small_fits(int rows, int cols);
+int launch_ortho_small(int dtype, const void* M, void* O, int mats, int rows, int cols, int steps,
+                       const float* coef, float scale, int32_t* status, cudaStream_t st);
 int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, int cols, int steps,
                          const float* coef, void* ws, int sms, cudaStream_t st);
 

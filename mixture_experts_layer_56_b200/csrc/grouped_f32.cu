@@ -1,10 +1,17 @@
 // fp32 products of ragged row groups with their group's matrix, on CUDA cores
 // (tensor cores have no fp32 multiply): forward, input and weight gradient.
 //
-// 64 x 64 tiles, 256 threads of 4 x 4 outputs, 16-deep slices in shared
-// memory.  Products are summed over 128 values at a time and these sums added
-// up apart, which keeps the rounding of long reductions near sqrt(128) rather
-// than sqrt(length) half steps.
+// 16 x 16 threads, MI x MI outputs each, 16-deep slices in two shared-memory
+// buffers: the next slice is on its way from global memory while one is
+// multiplied.  MI = 8 (128 x 128 tiles) reads 16 values from shared memory
+// per 64 multiply-adds and is bound by the fp32 pipe; MI = 4 (64 x 64 tiles)
+// is for shapes whose larger tiles would leave SMs idle or rows empty.
+// Multiply-adds are issued in pairs (fma.rn.f32x2, each lane rounded as an
+// fma.rn.f32).
+//
+// Products are summed over 128 values at a time and these sums added up apart,
+// which keeps the rounding of long reductions near sqrt(128) rather than
+// sqrt(length) half steps.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -14,11 +21,83 @@ namespace moe {
 
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 16;
+constexpr int TK = 16;
 constexpr int kFlush = 8;  // slices per inner sum
 constexpr int kMaxG = 256;
 
-template <int DIR>
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Four neighbours p[0..3], those at or past `left` zero.
+__device__ __forceinline__ float4 load4(const float* p, int left, bool vec) {
+  if (left >= 4 && vec) return *reinterpret_cast<const float4*>(p);
+  float4 v;
+  v.x = left > 0 ? p[0] : 0.0f;
+  v.y = left > 1 ? p[1] : 0.0f;
+  v.z = left > 2 ? p[2] : 0.0f;
+  v.w = left > 3 ? p[3] : 0.0f;
+  return v;
+}
+
+// An operand's slices: T rows (of D's M or N) by 16 reduction steps.  ALONG_R:
+// its memory rows run along the reduction, else along M (or N).
+template <int T, bool ALONG_R>
+struct Slice {
+  static constexpr int V = T * TK / 4 / 256;  // float4s per thread
+  float4 v[V];
+  // base: the tile's first element; rows, left: what remains of the tile's
+  // extent and of the reduction
+  __device__ __forceinline__ void load(const float* base, int64_t ld, int rows, int left, bool vec,
+                                       int tid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = tid + i * 256;
+      if (ALONG_R) {
+        const int row = e >> 2, r = (e & 3) * 4;
+        v[i] = load4(base + row * ld + r, row < rows ? left - r : 0, vec);
+      } else {
+        const int r = e / (T / 4), m = e % (T / 4) * 4;
+        v[i] = load4(base + r * ld + m, r < left ? rows - m : 0, vec);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(float (*s)[T + 4], int tid) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = tid + i * 256;
+      if (ALONG_R) {
+        const int row = e >> 2, r = (e & 3) * 4;
+        s[r][row] = v[i].x;
+        s[r + 1][row] = v[i].y;
+        s[r + 2][row] = v[i].z;
+        s[r + 3][row] = v[i].w;
+      } else {
+        const int r = e / (T / 4), m = e % (T / 4) * 4;
+        *reinterpret_cast<float4*>(&s[r][m]) = v[i];
+      }
+    }
+  }
+};
+
+template <int DIR, int MI>
 __global__ void __launch_bounds__(256)
 grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
                    const int32_t* __restrict__ offsets, int groups, int rows, int n, int k,
@@ -27,31 +106,49 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
   //   forward  M rows of X (ld k),  N rows of W_g (ld k),    r over k
   //   dX       M rows of dY (ld n), N columns of W_g (ld k), r over n
   //   dW       M columns of dY,     N columns of X,          r over the rows
-  __shared__ float As[TK][TM + 4];
-  __shared__ float Bs[TK][TN + 4];
+  constexpr int T = 16 * MI;
+  constexpr bool FWD = DIR == kGroupedFwd, DX = DIR == kGroupedDx, DW = DIR == kGroupedDw;
+  __shared__ __align__(16) float As[2][TK][T + 4];
+  __shared__ __align__(16) float Bs[2][TK][T + 4];
   __shared__ int32_t tile_start[kMaxG + 1];
   __shared__ int32_t row0s[kMaxG], rowsg[kMaxG];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  const int N = DIR == kGroupedFwd ? n : k;
-  const int nt = (N + TN - 1) / TN;
-  const int mt_dw = (n + TM - 1) / TM;
+  const int N = FWD ? n : k;
+  const int nt = (N + T - 1) / T;
+  const int mt_dw = (n + T - 1) / T;
   for (int g = tid; g < groups; g += 256) {
     const int p = min(max(offsets[g], 0), rows);
     const int e = min(max(offsets[g + 1], p), rows);
     row0s[g] = p;
     rowsg[g] = e - p;
-    tile_start[g + 1] = (DIR == kGroupedDw ? mt_dw : (e - p + TM - 1) / TM) * nt;
+    tile_start[g + 1] = (DW ? mt_dw : (e - p + T - 1) / T) * nt;
   }
   __syncthreads();
-  if (tid == 0) {
-    tile_start[0] = 0;
-    for (int g = 0; g < groups; ++g) tile_start[g + 1] += tile_start[g];
+  if (tid < 32) {
+    // inclusive scan, a run of groups per lane
+    const int per = (groups + 31) / 32, beg = min(tid * per, groups), end = min(beg + per, groups);
+    int sum = 0;
+    for (int i = beg; i < end; ++i) sum += tile_start[i + 1];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (tid >= o) incl += v;
+    }
+    int run = incl - sum;
+    for (int i = beg; i < end; ++i) {
+      run += tile_start[i + 1];
+      tile_start[i + 1] = run;
+    }
+    if (tid == 0) tile_start[0] = 0;
   }
   __syncthreads();
   const int total = tile_start[groups];
   const int tx = tid & 15, ty = tid >> 4;
+  const int64_t lda = FWD ? k : n, ldb = k;
+  const bool vec_a = lda % 4 == 0, vec_b = ldb % 4 == 0;
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     int lo = 0, hi = groups - 1;
     while (lo < hi) {
@@ -60,77 +157,96 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
     }
     const int g = lo;
     const int local = tile - tile_start[g];
-    const int m0 = (local / nt) * TM, n0 = (local % nt) * TN;
+    const int m0 = (local / nt) * T, n0 = (local % nt) * T;
     const int64_t r0 = row0s[g];
-    const int M = DIR == kGroupedDw ? n : rowsg[g];
-    const int R = DIR == kGroupedFwd ? k : (DIR == kGroupedDx ? n : rowsg[g]);
-    const float* wg = DIR == kGroupedDw ? nullptr : b + static_cast<int64_t>(g) * n * k;
-    float acc[4][4] = {}, sum[4][4] = {};
-    for (int rb = 0, cnt = 0; rb < R; rb += TK) {
+    const int M = DW ? n : rowsg[g];
+    const int R = FWD ? k : (DX ? n : rowsg[g]);
+    const float* wg = DW ? nullptr : b + static_cast<int64_t>(g) * n * k;
+    const float* pa = DW ? a + r0 * n + m0 : a + (r0 + m0) * lda;
+    const float* pb = FWD ? wg + static_cast<int64_t>(n0) * k : (DX ? wg + n0 : b + r0 * k + n0);
+    const int64_t step_a = DW ? lda * TK : TK, step_b = FWD ? TK : ldb * TK;
+    Slice<T, !DW> sa;
+    Slice<T, FWD> sb;
+    uint64_t acc[MI][MI / 2], sum[MI][MI / 2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = tid + i * 256;  // 1024 values of each operand
-        {
-          // consecutive threads follow the operand's memory rows
-          const int mm = DIR == kGroupedDw ? (e & 63) : (e >> 4);
-          const int rr = DIR == kGroupedDw ? (e >> 6) : (e & 15);
-          float v = 0.0f;
-          if (m0 + mm < M && rb + rr < R) {
-            if (DIR == kGroupedDw) v = a[(r0 + rb + rr) * n + m0 + mm];
-            else v = a[(r0 + m0 + mm) * (DIR == kGroupedFwd ? k : n) + rb + rr];
-          }
-          As[rr][mm] = v;
-        }
-        {
-          const int nn = DIR == kGroupedFwd ? (e >> 4) : (e & 63);
-          const int rr = DIR == kGroupedFwd ? (e & 15) : (e >> 6);
-          float v = 0.0f;
-          if (n0 + nn < N && rb + rr < R) {
-            if (DIR == kGroupedFwd) v = wg[static_cast<int64_t>(n0 + nn) * k + rb + rr];
-            else if (DIR == kGroupedDx) v = wg[static_cast<int64_t>(rb + rr) * k + n0 + nn];
-            else v = b[(r0 + rb + rr) * k + n0 + nn];
-          }
-          Bs[rr][nn] = v;
-        }
-      }
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < MI / 2; ++j) acc[i][j] = sum[i][j] = 0;
+    if (R > 0) {
+      sa.load(pa, lda, M - m0, R, vec_a, tid);
+      sb.load(pb, ldb, N - n0, R, vec_b, tid);
+    }
+    int buf = 0, cnt = 0;
+    for (int rb = 0; rb < R; rb += TK, buf ^= 1) {
+      sa.put(As[buf], tid);
+      sb.put(Bs[buf], tid);
+      // the slice before last is behind this barrier, and its buffer free
       __syncthreads();
+      if (rb + TK < R) {
+        pa += step_a;
+        pb += step_b;
+        sa.load(pa, lda, M - m0, R - rb - TK, vec_a, tid);
+        sb.load(pb, ldb, N - n0, R - rb - TK, vec_b, tid);
+      }
 #pragma unroll
       for (int r = 0; r < TK; ++r) {
-        const float4 x = *reinterpret_cast<const float4*>(&As[r][ty * 4]);
-        const float4 y = *reinterpret_cast<const float4*>(&Bs[r][tx * 4]);
-        const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+        // outputs ty*4 + i (+ 64), tx*4 + j (+ 64)
+        float x[MI];
+        uint64_t y[MI / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int h = 0; h < MI / 4; ++h) {
+          const float4 xv = *reinterpret_cast<const float4*>(&As[buf][r][h * 64 + ty * 4]);
+          x[h * 4] = xv.x; x[h * 4 + 1] = xv.y; x[h * 4 + 2] = xv.z; x[h * 4 + 3] = xv.w;
+          const ulonglong2 yv = *reinterpret_cast<const ulonglong2*>(&Bs[buf][r][h * 64 + tx * 4]);
+          y[h * 2] = yv.x;
+          y[h * 2 + 1] = yv.y;
+        }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xv[i], yv[j], acc[i][j]);
+        for (int i = 0; i < MI; ++i) {
+          const uint64_t xx = pack2(x[i], x[i]);
+#pragma unroll
+          for (int j = 0; j < MI / 2; ++j) acc[i][j] = fma2(xx, y[j], acc[i][j]);
+        }
       }
       if (++cnt == kFlush) {
         cnt = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sum[i][j] += acc[i][j];
-            acc[i][j] = 0.0f;
+          for (int j = 0; j < MI / 2; ++j) {
+            sum[i][j] = add2(sum[i][j], acc[i][j]);
+            acc[i][j] = 0;
           }
       }
-      __syncthreads();
     }
+    __syncthreads();  // the next tile writes buffer 0 again
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = m0 + ty * 4 + i;
+    for (int i = 0; i < MI; ++i) {
+      const int m = m0 + (i >> 2) * 64 + ty * 4 + (i & 3);
       if (m >= M) continue;
-      float* row = DIR == kGroupedDw ? out + (static_cast<int64_t>(g) * n + m) * k
-                                     : out + (r0 + m) * N;
+      float* row = DW ? out + (static_cast<int64_t>(g) * n + m) * k : out + (r0 + m) * N;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = n0 + tx * 4 + j;
-        if (c >= N) continue;
-        const float v = sum[i][j] + acc[i][j];
-        row[c] = accumulate ? row[c] + v : v;
+      for (int j = 0; j < MI / 2; ++j) {
+        const int c = n0 + (j >> 1) * 64 + tx * 4 + (j & 1) * 2;
+        const float2 v = unpack2(add2(sum[i][j], acc[i][j]));
+        if (c < N) row[c] = accumulate ? row[c] + v.x : v.x;
+        if (c + 1 < N) row[c + 1] = accumulate ? row[c + 1] + v.y : v.y;
       }
     }
   }
+}
+
+template <int MI>
+int launch_tiles(int dir, const float* a, const float* b, const int32_t* offsets, int groups,
+                 int64_t rows, int n, int k, float* out, bool accumulate, int64_t tiles, int most,
+                 cudaStream_t st) {
+  const int grid = static_cast<int>(tiles < most ? tiles : most);
+  if (grid <= 0) return MOE_OK;
+  auto kern = dir == kGroupedFwd ? grouped_f32_kernel<kGroupedFwd, MI>
+              : dir == kGroupedDx ? grouped_f32_kernel<kGroupedDx, MI>
+                                  : grouped_f32_kernel<kGroupedDw, MI>;
+  return launch_k(kern, dim3(grid), dim3(256), 0, st, 1, a, b, offsets, groups,
+                  static_cast<int>(rows), n, k, out, accumulate);
 }
 
 }  // namespace
@@ -138,18 +254,20 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
 int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* offsets, int groups,
                        int64_t rows, int n, int k, float* out, bool accumulate, int sms,
                        cudaStream_t st) {
-  const int N = dir == kGroupedFwd ? n : k;
-  const int64_t nt = (N + TN - 1) / TN;
-  const int64_t mt = dir == kGroupedDw ? static_cast<int64_t>(groups) * ((n + TM - 1) / TM)
-                                       : (rows + TM - 1) / TM + (rows < groups ? rows : groups);
-  const int64_t tiles = mt * nt, most = 4ll * sms;
-  const int grid = static_cast<int>(tiles < most ? tiles : most);
-  if (grid <= 0) return MOE_OK;
-  auto kern = dir == kGroupedFwd ? grouped_f32_kernel<kGroupedFwd>
-              : dir == kGroupedDx ? grouped_f32_kernel<kGroupedDx>
-                                  : grouped_f32_kernel<kGroupedDw>;
-  return launch_k(kern, dim3(grid), dim3(256), 0, st, 1, a, b, offsets, groups,
-                  static_cast<int>(rows), n, k, out, accumulate);
+  const int64_t N = dir == kGroupedFwd ? n : k;
+  const int64_t some = rows < groups ? rows : groups;  // groups with rows, at most
+  auto tiles = [&](int T) {
+    const int64_t nt = (N + T - 1) / T;
+    return nt * (dir == kGroupedDw ? static_cast<int64_t>(groups) * ((n + T - 1) / T)
+                                   : (rows + T - 1) / T + some);
+  };
+  // 128 x 128 tiles where they give every SM one and groups fill them
+  const bool fill = dir == kGroupedDw || rows >= 96 * some;
+  if (fill && tiles(128) >= sms)
+    return launch_tiles<8>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(128),
+                           sms, st);
+  return launch_tiles<4>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(64),
+                         3 * sms, st);
 }
 
 }  // namespace moe

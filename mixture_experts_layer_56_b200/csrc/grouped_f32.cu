@@ -9,9 +9,11 @@
 // Multiply-adds are issued in pairs (fma.rn.f32x2, each lane rounded as an
 // fma.rn.f32).
 //
-// Products are summed over 128 values at a time and these sums added up apart,
-// which keeps the rounding of long reductions near sqrt(128) rather than
-// sqrt(length) half steps.
+// The weight gradient, whose reduction is a group's rows, sums 128 products at
+// a time and adds these sums up apart, which keeps the rounding of long groups
+// near sqrt(128) rather than sqrt(rows) half steps.  The other two sum a
+// matrix's width in one chain, as two blocks per SM leave no registers for
+// more (8 x 1024 x 2048 x 1024: 49 TFLOP/s, with apart sums 46).
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -98,7 +100,7 @@ struct Slice {
 };
 
 template <int DIR, int MI>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, (MI == 8 && DIR != kGroupedDw) ? 2 : 1)
 grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
                    const int32_t* __restrict__ offsets, int groups, int rows, int n, int k,
                    float* __restrict__ out, bool accumulate) {
@@ -208,7 +210,7 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
           for (int j = 0; j < MI / 2; ++j) acc[i][j] = fma2(xx, y[j], acc[i][j]);
         }
       }
-      if (++cnt == kFlush) {
+      if (DW && ++cnt == kFlush) {
         cnt = 0;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
@@ -228,7 +230,7 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
 #pragma unroll
       for (int j = 0; j < MI / 2; ++j) {
         const int c = n0 + (j >> 1) * 64 + tx * 4 + (j & 1) * 2;
-        const float2 v = unpack2(add2(sum[i][j], acc[i][j]));
+        const float2 v = unpack2(DW ? add2(sum[i][j], acc[i][j]) : acc[i][j]);
         if (c < N) row[c] = accumulate ? row[c] + v.x : v.x;
         if (c + 1 < N) row[c + 1] = accumulate ? row[c + 1] + v.y : v.y;
       }
@@ -261,11 +263,12 @@ int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* o
     return nt * (dir == kGroupedDw ? static_cast<int64_t>(groups) * ((n + T - 1) / T)
                                    : (rows + T - 1) / T + some);
   };
-  // 128 x 128 tiles where they give every SM one and groups fill them
+  // 128 x 128 tiles where they give every SM one and groups fill them (two
+  // blocks of them per SM, or one where the sums apart take the registers)
   const bool fill = dir == kGroupedDw || rows >= 96 * some;
   if (fill && tiles(128) >= sms)
     return launch_tiles<8>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(128),
-                           sms, st);
+                           dir == kGroupedDw ? sms : 2 * sms, st);
   return launch_tiles<4>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(64),
                          3 * sms, st);
 }

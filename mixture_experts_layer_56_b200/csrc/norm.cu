@@ -6,7 +6,7 @@
 //   dgamma = sum_t dy h,  dbeta = sum_t dy
 //
 // Bound by memory.  A row is read once and held in registers: a group of
-// 32..512 threads per row, kVals values each, so that the variance is taken
+// 32 to 512 threads per row, kVals values each, so that the variance is taken
 // about the mean (a second pass over registers) rather than as a difference of
 // sums.  The backward pass runs a fixed set of blocks over all rows; a thread
 // keeps the same columns for every row and carries their dgamma and dbeta sums
@@ -22,99 +22,177 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxGroup = 512;  // threads per row
-
 template <typename T> struct NormCfg;
 template <> struct NormCfg<bf16> { static constexpr int kVals = 16; };
 template <> struct NormCfg<float> { static constexpr int kVals = 8; };
 
-// A thread's kVals values of a row: 16-byte pieces t, t + TPR, ... (VEC) or
-// single elements t, t + TPR, ...; those past the row are 0.
+// Pairs of fp32 values in 64-bit registers: Blackwell's packed arithmetic
+// halves the instructions, of which these kernels have as many as the memory
+// leaves time for.  Each half is rounded as by the scalar instruction.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 pair(float x, float y) {
+  F2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ float2 both(F2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float sum_of(F2 v) {
+  const float2 f = both(v);
+  return f.x + f.y;
+}
+
+// A 16-byte piece as pairs.
+__device__ __forceinline__ void piece_pairs(const uint4& w, F2* v, bf16) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = pair(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void piece_pairs(const uint4& w, F2* v, float) {
+  v[0] = pair(__uint_as_float(w.x), __uint_as_float(w.y));
+  v[1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
+}
+__device__ __forceinline__ uint4 pairs_piece(const F2* v, bf16) {
+  uint4 w;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = both(v[i]);
+    h[i] = __floats2bfloat162_rn(f.x, f.y);
+  }
+  return w;
+}
+__device__ __forceinline__ uint4 pairs_piece(const F2* v, float) {
+  const float2 a = both(v[0]), b = both(v[1]);
+  return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                    __float_as_uint(b.y));
+}
+
+// A thread's kVals values of a row, as kVals / 2 pairs: 16-byte pieces t,
+// t + TPR, ... (VEC) or single elements t, t + TPR, ...; those past the row
+// are 0.
 template <typename T, bool VEC>
 struct RowSlice {
   static constexpr int V = NormCfg<T>::kVals;
   static constexpr int N = Vec16<T>::N;
   static constexpr int P = V / N;
+  static constexpr int PP = N / 2;  // pairs of a piece
 
   // column of value i
   __device__ __forceinline__ static int col(int i, int t, int tpr) {
     return VEC ? (t + (i / N) * tpr) * N + i % N : t + i * tpr;
   }
-  template <typename S>
-  __device__ __forceinline__ static void load_f32(const S* p, int d, int t, int tpr, float fill,
-                                                  float* v) {
-    if (VEC && sizeof(S) == 4) {
-      // a piece is 4 or 8 neighbours: whole 16-byte loads
+  // fp32 parameters
+  __device__ __forceinline__ static void load_f32(const float* p, int d, int t, int tpr, F2* v) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const int c = col(i, t, tpr);
-        if (c < d) {
-          Vec16<float>::load(reinterpret_cast<const float*>(p) + c, v + i);
-        } else {
-          v[i] = v[i + 1] = v[i + 2] = v[i + 3] = fill;
-        }
-      }
-    } else {
+    for (int i = 0; i < V; i += 4) {
+      float f[4] = {};
+      const int c = col(i, t, tpr);
+      if (VEC) {
+        if (c < d) Vec16<float>::load(p + c, f);
+      } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = col(i, t, tpr);
-        v[i] = c < d ? to_f32(p[c]) : fill;
+        for (int j = 0; j < 4; ++j)
+          if (c + j * tpr < d) f[j] = p[c + j * tpr];
       }
+      v[i / 2] = pair(f[0], f[1]);
+      v[i / 2 + 1] = pair(f[2], f[3]);
     }
   }
-  __device__ __forceinline__ static void load(const T* p, int d, int t, int tpr, float* v) {
+  __device__ __forceinline__ static void load(const T* p, int d, int t, int tpr, F2* v) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const int c = col(i, t, tpr), e = col(i + 1, t, tpr);
+      v[i / 2] = pair(c < d ? to_f32(p[c]) : 0.0f, e < d ? to_f32(p[e]) : 0.0f);
+    }
+  }
+  __device__ __forceinline__ static void store(T* p, int d, int t, int tpr, const F2* v) {
     if (VEC) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         const int c = (t + i * tpr) * N;
-        if (c < d) {
-          Vec16<T>::load(p + c, v + i * N);
-        } else {
-#pragma unroll
-          for (int j = 0; j < N; ++j) v[i * N + j] = 0.0f;
-        }
+        if (c < d) *reinterpret_cast<uint4*>(p + c) = pairs_piece(v + i * PP, T());
       }
     } else {
-      load_f32(p, d, t, tpr, 0.0f, v);
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const int c = col(i, t, tpr), e = col(i + 1, t, tpr);
+        const float2 f = both(v[i / 2]);
+        if (c < d) p[c] = from_f32<T>(f.x);
+        if (e < d) p[e] = from_f32<T>(f.y);
+      }
     }
   }
-  __device__ __forceinline__ static void store(T* p, int d, int t, int tpr, const float* v) {
+  // zeroes the values past the row
+  __device__ __forceinline__ static void clip(int d, int t, int tpr, F2* v) {
     if (VEC) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int c = (t + i * tpr) * N;
-        if (c < d) Vec16<T>::store(p + c, v + i * N);
-      }
+      for (int i = 0; i < P; ++i)
+        if ((t + i * tpr) * N >= d) {
+#pragma unroll
+          for (int j = 0; j < PP; ++j) v[i * PP + j] = 0;
+        }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = col(i, t, tpr);
-        if (c < d) p[c] = from_f32<T>(v[i]);
+      for (int i = 0; i < V; i += 2) {
+        const float2 f = both(v[i / 2]);
+        v[i / 2] = pair(col(i, t, tpr) < d ? f.x : 0.0f, col(i + 1, t, tpr) < d ? f.y : 0.0f);
       }
     }
+  }
+  // how many values lie in the row
+  __device__ __forceinline__ static int count(int d, int t, int tpr) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) n += col(i, t, tpr) < d;
+    return n;
   }
 };
 
-// Sum over the group of TPR threads that holds this thread (every thread of
-// the block calls it; `red` is used by no other call until a block barrier).
-template <int TPR>
-__device__ __forceinline__ float group_sum(float v, float* red) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (TPR > 32) {
-    constexpr int W = TPR / 32;
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    const int w0 = warp / W * W;
-    v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) v += red[w0 + i];
-  }
   return v;
 }
 
-template <int TPR> constexpr int block_of() { return TPR > 256 ? TPR : 256; }
+// Sum over a block of 512 threads (`red` is used by no other call until a
+// block barrier).
+__device__ __forceinline__ float block_sum512(float v, float* red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v += red[i];
+  return v;
+}
+
+// Threads of a block: whole groups, about 256; and the blocks that the
+// registers let an SM hold in the forward and the backward kernel.
+constexpr int block_threads(int tpr) { return tpr > 256 ? tpr : 256 / tpr * tpr; }
+template <int TPR> constexpr int block_of() { return block_threads(TPR); }
+constexpr int at_least_1(int v) { return v > 1 ? v : 1; }
+constexpr int fwd_blocks(int tpr) { return at_least_1(768 / block_threads(tpr)); }
+constexpr int bwd_blocks(int tpr) { return at_least_1(512 / block_threads(tpr)); }
 
 // Rows on their way from memory: kRing rows per group, of each of the ARRAYS
 // that a pass reads, in shared memory, fetched with cp.async.  A thread copies exactly the values that it
@@ -169,40 +247,41 @@ struct RowRing {
     }
   }
   __device__ __forceinline__ static void take(uint8_t* base, int stage, int which, int d, int t,
-                                              float* v) {
+                                              F2* v) {
     if (VEC) {
 #pragma unroll
       for (int i = 0; i < S::P; ++i) {
-        if ((t + i * TPR) * S::N < d) {
-          Vec16<T>::load(slot(base, stage, which, i), v + i * S::N);
-        } else {
-#pragma unroll
-          for (int j = 0; j < S::N; ++j) v[i * S::N + j] = 0.0f;
-        }
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if ((t + i * TPR) * S::N < d)
+          w = *reinterpret_cast<const uint4*>(slot(base, stage, which, i));
+        piece_pairs(w, v + i * S::PP, T());
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < S::V; ++i)
-        v[i] = t + i * TPR < d ? to_f32(*slot(base, stage, which, i)) : 0.0f;
+      for (int i = 0; i < S::V; i += 2)
+        v[i / 2] = pair(t + i * TPR < d ? to_f32(*slot(base, stage, which, i)) : 0.0f,
+                        t + (i + 1) * TPR < d ? to_f32(*slot(base, stage, which, i + 1)) : 0.0f);
     }
   }
 };
 
 template <typename T, bool VEC, int TPR>
-__global__ void __launch_bounds__(block_of<TPR>(), TPR > 256 ? 1 : 3)
+__global__ void __launch_bounds__(block_of<TPR>(), fwd_blocks(TPR))
 norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __restrict__ beta,
                 int64_t rows, int d, float eps, T* y, float* __restrict__ mean,
                 float* __restrict__ rstd) {
   using S = RowSlice<T, VEC>;
   using R = RowRing<T, VEC, TPR, 1>;
-  constexpr int V = S::V;
+  constexpr int H = S::V / 2;
   constexpr int RG = block_of<TPR>() / TPR;
+  constexpr int W = TPR / 32;  // warps per row
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float red[2][block_of<TPR>() / 32];
+  __shared__ float2 red[2][block_of<TPR>() / 32];
   pdl_wait();
   pdl_trigger();
   const int t = threadIdx.x % TPR;
   const int grp = threadIdx.x / TPR;
+  const int warp = threadIdx.x >> 5, w0 = warp / W * W;
   const int64_t step = static_cast<int64_t>(gridDim.x) * RG;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * RG + grp;
   auto fetch = [&](int64_t row, int stage) {
@@ -211,20 +290,31 @@ norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __rest
   };
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) fetch(first + s * step, s);
-  float g[V], b[V];
-  S::load_f32(gamma, d, t, TPR, 0.0f, g);
-  if (beta != nullptr) {
-    S::load_f32(beta, d, t, TPR, 0.0f, b);
-  } else {
+  F2 g[H], b[H];
+  S::load_f32(gamma, d, t, TPR, g);
 #pragma unroll
-    for (int i = 0; i < V; ++i) b[i] = 0.0f;
+  for (int i = 0; i < H; ++i) b[i] = 0;
+  if (beta != nullptr) S::load_f32(beta, d, t, TPR, b);
+  const float inv_d = 1.0f / d;
+  // values of a row in this warp, and what turns their sum into their mean
+  const float n_w = warp_sum(static_cast<float>(S::count(d, t, TPR)));
+  const float inv_n = n_w > 0.0f ? 1.0f / n_w : 0.0f;
+  float n_of[W];  // and in each warp of the row
+  if (W > 1) {
+    if ((threadIdx.x & 31) == 0) red[0][warp].x = n_w;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) n_of[i] = red[0][w0 + i].x;
+    __syncthreads();
   }
-  int stage = 0;
+  int stage = 0, buf = 0;
   // every group of the block takes the same number of turns
-  for (int64_t row = first; row - grp < rows; row += step) {
+  for (int64_t row = first; row - grp < rows; row += step, buf ^= 1) {
     const bool live = row < rows;
     fetch(row + (kRing - 1) * step, (stage + kRing - 1) % kRing);
-    float v[V];
+    F2 v[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) v[i] = 0;
     if (live) {
       if (R::kAsync) {
         copy_wait<kRing - 1>();
@@ -232,25 +322,48 @@ norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __rest
       } else {
         S::load(x + row * d, d, t, TPR, v);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = 0.0f;
     }
     stage = (stage + 1) % kRing;
-    float s = 0.0f;
+    // each warp takes its values' mean and squares about it, and the warps of
+    // a row then join theirs: M2 = sum M2_w + n_w (mean_w - mean)^2.  One
+    // barrier, and no difference of large sums.
+    F2 s = v[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) s += v[i];
-    const float mu = group_sum<TPR>(s, red[0]) / d;
-    float q = 0.0f;
+    for (int i = 1; i < H; ++i) s = add(s, v[i]);
+    const float mu_w = warp_sum(sum_of(s)) * inv_n;
+    float mu = mu_w;
+    F2 m = pair(-mu, -mu);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[i] = S::col(i, t, TPR) < d ? v[i] - mu : 0.0f;
-      q += v[i] * v[i];
+    for (int i = 0; i < H; ++i) v[i] = add(v[i], m);
+    S::clip(d, t, TPR, v);
+    F2 q = mul(v[0], v[0]);
+#pragma unroll
+    for (int i = 1; i < H; ++i) q = fma2(v[i], v[i], q);
+    float m2 = warp_sum(sum_of(q));
+    if (W > 1) {
+      if ((threadIdx.x & 31) == 0) red[buf][warp] = make_float2(mu, m2);
+      __syncthreads();
+      float2 of[W];
+      float all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        of[i] = red[buf][w0 + i];
+        all += n_of[i] * (of[i].x - of[0].x);
+      }
+      mu = of[0].x + all * inv_d;  // of the row
+      m2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float e = of[i].x - mu;
+        m2 += of[i].y + n_of[i] * (e * e);
+      }
     }
-    const float rs = 1.0f / sqrtf(group_sum<TPR>(q, red[1]) / d + eps);
+    const float rs = 1.0f / sqrtf(m2 * inv_d + eps);
     if (!live) continue;
+    m = pair(mu_w - mu, mu_w - mu);  // v is about the warp's mean already
+    const F2 r2 = pair(rs, rs);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = v[i] * rs * g[i] + b[i];
+    for (int i = 0; i < H; ++i) v[i] = fma2(mul(add(v[i], m), r2), g[i], b[i]);
     S::store(y + row * d, d, t, TPR, v);
     if (t == 0) {
       if (mean != nullptr) mean[row] = mu;
@@ -272,13 +385,13 @@ norm_fwd_wide_kernel(const T* x, const float* __restrict__ gamma,
   const T* p = x + row * d;
   float s = 0.0f;
   for (int c = threadIdx.x; c < d; c += 512) s += to_f32(p[c]);
-  const float mu = group_sum<512>(s, red[0]) / d;
+  const float mu = block_sum512(s, red[0]) / d;
   float q = 0.0f;
   for (int c = threadIdx.x; c < d; c += 512) {
     const float h = to_f32(p[c]) - mu;
     q += h * h;
   }
-  const float rs = 1.0f / sqrtf(group_sum<512>(q, red[1]) / d + eps);
+  const float rs = 1.0f / sqrtf(block_sum512(q, red[1]) / d + eps);
   for (int c = threadIdx.x; c < d; c += 512) {
     const float h = (to_f32(p[c]) - mu) * rs * gamma[c];
     y[row * d + c] = from_f32<T>(beta != nullptr ? h + beta[c] : h);
@@ -297,13 +410,13 @@ constexpr int bwd_smem() {
 }
 
 template <typename T, bool VEC, int TPR>
-__global__ void __launch_bounds__(block_of<TPR>(), TPR > 256 ? 1 : 2)
+__global__ void __launch_bounds__(block_of<TPR>(), bwd_blocks(TPR))
 norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ gamma,
                 const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows,
                 int d, T* dx, float* __restrict__ part) {
   using S = RowSlice<T, VEC>;
   using R = RowRing<T, VEC, TPR, 2>;
-  constexpr int V = S::V;
+  constexpr int V = S::V, H = V / 2;
   constexpr int B = block_of<TPR>();
   constexpr int RG = B / TPR;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -323,10 +436,10 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
   };
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) fetch(first + s * step, s);
-  float g[V], dg[V], db[V];
-  S::load_f32(gamma, d, t, TPR, 0.0f, g);
+  F2 g[H], dg[H], db[H];
+  S::load_f32(gamma, d, t, TPR, g);
 #pragma unroll
-  for (int i = 0; i < V; ++i) dg[i] = db[i] = 0.0f;
+  for (int i = 0; i < H; ++i) dg[i] = db[i] = 0;
   const float inv_d = 1.0f / d;
   float mu = 0.0f, rs = 0.0f;
   if (first < rows) {
@@ -343,7 +456,9 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
       mu_next = mean[row + step];
       rs_next = rstd[row + step];
     }
-    float h[V], v[V];
+    F2 h[H], v[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) h[i] = v[i] = 0;
     if (live) {
       if (R::kAsync) {
         copy_wait<kRing - 1>();
@@ -353,22 +468,21 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
         S::load(x + row * d, d, t, TPR, h);
         S::load(dy + row * d, d, t, TPR, v);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = v[i] = 0.0f;
     }
     stage = (stage + 1) % kRing;
-    float s1 = 0.0f, s2 = 0.0f;
+    const F2 m = pair(-mu, -mu), r2 = pair(rs, rs);
+    F2 a1 = 0, a2 = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < H; ++i) {
       // past the row dy and gamma are 0, and h is not used
-      h[i] = (h[i] - mu) * rs;
-      dg[i] += v[i] * h[i];
-      db[i] += v[i];
-      v[i] *= g[i];
-      s1 += v[i];
-      s2 += v[i] * h[i];
+      h[i] = mul(add(h[i], m), r2);
+      dg[i] = fma2(v[i], h[i], dg[i]);
+      db[i] = add(db[i], v[i]);
+      v[i] = mul(v[i], g[i]);
+      a1 = add(a1, v[i]);
+      a2 = fma2(v[i], h[i], a2);
     }
+    float s1 = sum_of(a1), s2 = sum_of(a2);
     // one barrier for both sums: the next row's use of this buffer is behind
     // the barrier of the row between
 #pragma unroll
@@ -392,11 +506,11 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
         s2 += red[buf][1][w0 + i];
       }
     }
-    s1 *= inv_d;
-    s2 *= inv_d;
     if (live) {
+      // s (v - s1 - h s2)
+      const F2 c1 = pair(-s1 * inv_d, -s1 * inv_d), c2 = pair(-s2 * inv_d, -s2 * inv_d);
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = rs * (v[i] - s1 - h[i] * s2);
+      for (int i = 0; i < H; ++i) v[i] = mul(r2, fma2(h[i], c2, add(v[i], c1)));
       S::store(dx + row * d, d, t, TPR, v);
     }
     mu = mu_next;
@@ -405,13 +519,22 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
   // this block's sums: part[0] dgamma, part[1] dbeta, [gridDim.x, d] each
   float* pg = part + static_cast<int64_t>(blockIdx.x) * d;
   float* pb = part + (static_cast<int64_t>(gridDim.x) + blockIdx.x) * d;
+  float dgf[V], dbf[V];
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    const float2 p = both(dg[i]), o = both(db[i]);
+    dgf[2 * i] = p.x;
+    dgf[2 * i + 1] = p.y;
+    dbf[2 * i] = o.x;
+    dbf[2 * i + 1] = o.y;
+  }
   if (RG == 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = S::col(i, t, TPR);
       if (c < d) {
-        pg[c] = dg[i];
-        pb[c] = db[i];
+        pg[c] = dgf[i];
+        pb[c] = dbf[i];
       }
     }
   } else {
@@ -423,7 +546,7 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = S::col(i, t, TPR);
-        if (c < d) acc[grp * TPR * V + c] = pass ? db[i] : dg[i];
+        if (c < d) acc[grp * TPR * V + c] = pass ? dbf[i] : dgf[i];
       }
       __syncthreads();
       for (int c = threadIdx.x; c < d; c += B) {
@@ -453,8 +576,8 @@ norm_bwd_wide_kernel(const T* dy, const T* __restrict__ x,
     s1 += v;
     s2 += v * ((to_f32(x[row * d + c]) - mu) * rs);
   }
-  s1 = group_sum<512>(s1, red[0]) / d;
-  s2 = group_sum<512>(s2, red[1]) / d;
+  s1 = block_sum512(s1, red[0]) / d;
+  s2 = block_sum512(s2, red[1]) / d;
   for (int c = threadIdx.x; c < d; c += 512) {
     const float v = to_f32(dy[row * d + c]) * gamma[c];
     const float h = (to_f32(x[row * d + c]) - mu) * rs;
@@ -509,7 +632,7 @@ norm_bwd_reduce_kernel(const float* __restrict__ part, int part_rows, int d,
 // threads per row that hold d values, or 0 (too wide)
 template <typename T>
 int group_of(int d) {
-  for (int tpr = 32; tpr <= kMaxGroup; tpr *= 2)
+  for (int tpr : {32, 64, 96, 128, 192, 256, 384, 512})
     if (d <= tpr * NormCfg<T>::kVals) return tpr;
   return 0;
 }
@@ -518,9 +641,9 @@ template <typename T>
 int part_rows_of(int64_t T_, int d, int sms) {
   const int tpr = group_of<T>(d);
   if (tpr == 0) return static_cast<int>(T_ < 64 ? T_ : 64);
-  const int rg = tpr > 256 ? 1 : 256 / tpr;
+  const int rg = block_threads(tpr) / tpr;
   const int64_t blocks = (T_ + rg - 1) / rg;
-  const int64_t most = static_cast<int64_t>(sms) * (tpr > 256 ? 1 : 2);
+  const int64_t most = static_cast<int64_t>(sms) * bwd_blocks(tpr);
   return static_cast<int>(blocks < most ? blocks : most);
 }
 
@@ -532,7 +655,7 @@ int fwd_impl(const T* x, const float* gamma, const float* beta, int64_t rows, in
   static std::atomic<uint64_t> optin{0};
   auto kern = norm_fwd_kernel<T, VEC, TPR>;
   if (int rc = ensure_smem_optin(reinterpret_cast<const void*>(kern), smem, optin)) return rc;
-  const int64_t blocks = (rows + RG - 1) / RG, most = static_cast<int64_t>(sms) * (TPR > 256 ? 2 : 3);
+  const int64_t blocks = (rows + RG - 1) / RG, most = static_cast<int64_t>(sms) * fwd_blocks(TPR);
   return launch_k(kern, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
                   dim3(block_of<TPR>()), smem, st, 1, x, gamma, beta, rows, d, eps, y, mean, rstd);
 }
@@ -543,8 +666,11 @@ int fwd_group(const T* x, const float* gamma, const float* beta, int64_t rows, i
   switch (group_of<T>(d)) {
     case 32: return fwd_impl<T, VEC, 32>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
     case 64: return fwd_impl<T, VEC, 64>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
+    case 96: return fwd_impl<T, VEC, 96>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
     case 128: return fwd_impl<T, VEC, 128>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
+    case 192: return fwd_impl<T, VEC, 192>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
     case 256: return fwd_impl<T, VEC, 256>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
+    case 384: return fwd_impl<T, VEC, 384>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
     case 512: return fwd_impl<T, VEC, 512>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
   }
   return launch_k(norm_fwd_wide_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, 1,
@@ -576,8 +702,11 @@ int bwd_group(const T* dy, const T* x, const float* gamma, const float* mean, co
   switch (group_of<T>(d)) {
     case 32: return bwd_impl<T, VEC, 32>(dy, x, gamma, mean, rstd, rows, d, dx, part, part_rows, st);
     case 64: return bwd_impl<T, VEC, 64>(dy, x, gamma, mean, rstd, rows, d, dx, part, part_rows, st);
+    case 96: return bwd_impl<T, VEC, 96>(dy, x, gamma, mean, rstd, rows, d, dx, part, part_rows, st);
     case 128: return bwd_impl<T, VEC, 128>(dy, x, gamma, mean, rstd, rows, d, dx, part, part_rows, st);
+    case 192: return bwd_impl<T, VEC, 192>(dy, x, gamma, mean, rstd, rows, d, dx, part, part_rows, st);
     case 256: return bwd_impl<T, VEC, 256>(dy, x, gamma, mean, rstd, rows, d, dx, part, part_rows, st);
+    case 384: return bwd_impl<T, VEC, 384>(dy, x, gamma, mean, rstd, rows, d, dx, part, part_rows, st);
     case 512: return bwd_impl<T, VEC, 512>(dy, x, gamma, mean, rstd, rows, d, dx, part, part_rows, st);
   }
   // the column sums first: dx may be dy

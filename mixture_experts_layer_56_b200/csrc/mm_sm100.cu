@@ -46,6 +46,7 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kStagePitch = 128 + 16;  // staging row: 128 bytes, padded off the bank period
 constexpr int kWarpStage = 32 * kStagePitch;
+constexpr int kWarpDiag = 128 * 4;  // a diagonal's values over an epilogue warp's columns
 constexpr uint32_t kSliceBytes = 64 * kKB * 2;  // an MN-major 64-wide slice
 constexpr int kColChunk = 8;  // N tiles that a group's row blocks sweep together
 
@@ -57,8 +58,8 @@ struct Stage {
   static constexpr uint32_t kBytes = kA + kB;
   // what 227 KB hold beside the epilogue's staging and 5 KB of barriers,
   // group tables and alignment
-  static constexpr int kCount = (227 * 1024 - 5120 - kEpiWarps * kWarpStage) / kBytes;
-  static constexpr int kSmem = kCount * kBytes + kEpiWarps * kWarpStage + 1024;
+  static constexpr int kCount = (227 * 1024 - 5120 - kEpiWarps * (kWarpStage + kWarpDiag)) / kBytes;
+  static constexpr int kSmem = kCount * kBytes + kEpiWarps * (kWarpStage + kWarpDiag) + 1024;
   static_assert(kCount >= 4 && kCount <= 16, "the issued-stage masks hold 32");
 };
 
@@ -262,7 +263,11 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
   const int mt_fixed = RAG_M ? 0 : (args.m + kTile - 1) / kTile;
-  const int per_group = SYM ? mt_fixed * (mt_fixed + 1) / 2 : mt_fixed * nt;
+  // a symmetric product's block of rows mb has the column tiles up to its
+  // diagonal block, each 1 / per_blk of a block wide
+  const int per_blk = kTile / tn;
+  const int per_group =
+      SYM ? per_blk * (mt_fixed * (mt_fixed - 1) / 2) + nt : mt_fixed * nt;
   const int total_tiles = RAG_M ? tile_start[G] : G * per_group;
 
   // position v of this pair's sequence cluster, cluster + nclusters, ...
@@ -301,11 +306,12 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const int local = t - ti.g * per_group;
       if (RAG_K) ti.g = grp_order[ti.g];
       if (SYM) {
-        int mb = static_cast<int>((sqrtf(8.0f * local + 1.0f) - 1.0f) * 0.5f);
-        while (mb * (mb + 1) / 2 > local) --mb;
-        while ((mb + 1) * (mb + 2) / 2 <= local) ++mb;
+        const int blk = local / per_blk;
+        int mb = static_cast<int>((sqrtf(8.0f * blk + 1.0f) - 1.0f) * 0.5f);
+        while (mb * (mb + 1) / 2 > blk) --mb;
+        while ((mb + 1) * (mb + 2) / 2 <= blk) ++mb;
         ti.m_blk = mb;
-        ti.n_blk = local - mb * (mb + 1) / 2;
+        ti.n_blk = local - per_blk * (mb * (mb + 1) / 2);
       } else {
         ti.m_blk = local / nt;
         ti.n_blk = local - ti.m_blk * nt;
@@ -357,8 +363,11 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       // a CTA without rows leaves its part of A as it is: what the MMA makes
       // of it is not stored
       const bool mine = has_rows(ti, static_cast<int>(rank));
-      const uint32_t bytes = (mine ? A_BYTES : 0) + B_BYTES;
-      const uint32_t pair_bytes = 2 * B_BYTES + A_BYTES + (has_rows(ti, 1) ? A_BYTES : 0);
+      // of an MN-major B the slices that the tile's width takes
+      const bool two = !B_MN || ti.ncols > 128;
+      const uint32_t b_bytes = two ? B_BYTES : kSliceBytes;
+      const uint32_t bytes = (mine ? A_BYTES : 0) + b_bytes;
+      const uint32_t pair_bytes = 2 * b_bytes + A_BYTES + (has_rows(ti, 1) ? A_BYTES : 0);
       const int za = RAG_M || RAG_K ? 0 : ti.g;
       const int zb = RAG_K ? 0 : ti.g;
       int k0 = RAG_K ? ti.row0 : 0;
@@ -387,7 +396,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           }
           if (B_MN) {
             tma_load_3d_pair(sb, &tmB, fb, n0, k0, zb);
-            tma_load_3d_pair(sb + kSliceBytes, &tmB, fb, n0 + 64, k0, zb);
+            if (two) tma_load_3d_pair(sb + kSliceBytes, &tmB, fb, n0 + 64, k0, zb);
           } else {
             tma_load_3d_pair(sb, &tmB, fb, k0, n0, zb);
           }
@@ -496,6 +505,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     // ------------------------------------------------------- epilogue -----
     const int q = warp & 3;            // TMEM lane quarter of this warp
     const int hcol = (warp - 4) >> 2;  // which half of the tile's columns it drains
+    constexpr int CW = EPI == kMmStoreBf16 ? 64 : 32;  // columns of a chunk
+    const int hw = (tn / 2 + CW - 1) / CW * CW;        // columns of a half
     const int r = q * 32 + lane;
     const uint32_t tempty_leader0 = map_to_cta(tempty_bar(0), 0);
     const uint32_t tempty_leader1 = map_to_cta(tempty_bar(1), 0);
@@ -506,26 +517,58 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     constexpr bool SRC = EPI == kMmPoly || EPI == kMmUpdate;
     RowFetch src_hi[2], src_lo[2];
     auto fetch_src = [&](const Tile& t, int c) {
-      const int col = t.col0 + hcol * 128 + c * 32;
+      const int col = t.col0 + hcol * hw + c * 32;
       const int row0 = t.m_blk * kTile + static_cast<int>(rank) * kHalf + q * 32;
       const int64_t at = t.g * (static_cast<int64_t>(args.m) * args.ld) + row0 * args.ld + col;
-      const int rows = col < t.col0 + tn ? args.m - row0 : 0;
+      const int rows = c * 32 < hw && col < t.col0 + tn ? args.m - row0 : 0;
       const int pieces = (static_cast<int>(args.ld) - col) / 8;
       src_hi[c & 1].fetch(static_cast<const __half*>(args.src) + at, args.ld, rows, pieces, lane);
       if (EPI == kMmUpdate)
         src_lo[c & 1].fetch(static_cast<const __half*>(args.src_lo) + at, args.ld, rows, pieces,
                             lane);
     };
+    // and of the diagonal beside them: a value per row, or per column, which
+    // go to this warp's columns in shared memory
+    float* diag_cols =
+        reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES + kEpiWarps * kWarpStage) +
+        (warp - 4) * (kWarpDiag / 4);
+    const bool by_row = EPI == kMmPoly || !args.diag_cols, by_col = EPI == kMmPoly || args.diag_cols;
+    float next_row[4] = {};
+    float4 next_col = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto fetch_diag = [&](const Tile& t) {
+      const float* diag = args.diag + static_cast<int64_t>(t.g) * args.diag_ld;
+      const int row0 = t.m_blk * kTile + static_cast<int>(rank) * kHalf + q * 32;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int pr = row0 + i * 8 + lane / 4;
+        next_row[i] = by_row && pr < args.m ? diag[pr] : 0.0f;
+      }
+      const int col = t.col0 + hcol * hw + lane * 4;
+      next_col = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (by_col && col < args.diag_ld) next_col = *reinterpret_cast<const float4*>(diag + col);
+    };
     Tile following{};
     if (SRC && cluster < total_tiles) {
       following = tile_of(cluster);
+      fetch_diag(following);
       fetch_src(following, 0);
       fetch_src(following, 1);
     }
     for (int tile = cluster; tile < total_tiles; tile += nclusters) {
       const Tile ti = SRC ? following : tile_of(tile);
       const bool more = tile + nclusters < total_tiles;
-      if (SRC && more) following = tile_of(tile + nclusters);
+      float drow[4] = {};
+      if (SRC) {
+        __syncwarp();
+        *reinterpret_cast<float4*>(diag_cols + lane * 4) = next_col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) drow[i] = next_row[i];
+        __syncwarp();
+        if (more) {
+          following = tile_of(tile + nclusters);
+          fetch_diag(following);
+        }
+      }
       auto fetch_ahead = [&](int c) {
         if (c < 2) fetch_src(ti, c + 2);
         else if (more) fetch_src(following, c - 2);
@@ -561,16 +604,16 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       }
       const int row = ti.m_blk * kTile + static_cast<int>(rank) * kHalf + r;
       const bool live = row < (RAG_K ? args.m : ti.rows);
-      const int col0 = ti.col0 + hcol * 128;
-      const int col_end = min(ti.col0 + tn, args.n);
+      const int col0 = ti.col0 + hcol * hw;
+      const int col_end = min(min(col0 + hw, ti.col0 + tn), args.n);
       const int ld_end = col_end < args.n ? col_end : static_cast<int>(args.ld);
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                             static_cast<uint32_t>(acc * kTile + hcol * 128);
+                             static_cast<uint32_t>(acc * kTile + hcol * hw);
       const int64_t orow = RAG_M ? static_cast<int64_t>(ti.row0) + row : row;
       const int64_t obase = (RAG_M ? 0 : ti.g * args.out_stride) + orow * args.ld;
       if (EPI == kMmStoreBf16) {
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 2; ++c) {  // a half is at most 128 wide
           const int col = col0 + c * 64;
           if (col >= col_end) break;
           float x[64];
@@ -641,7 +684,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           __half* out = omat + static_cast<int64_t>(row) * args.ld + col;
           store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
                         (ld_end - col) / 8, lane, PutPlain{});
-          if (SYM && ti.m_blk != ti.n_blk) {
+          if (SYM && ti.m_blk != ti.n_blk / per_blk) {
             // the mirrored tile: lane r writes column r of the staging area,
             // whose rows go out in 16-byte pieces
 #pragma unroll
@@ -663,16 +706,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       } else if (EPI == kMmPoly) {
         // off the diagonal b a + c ((d_i + d_j) a + o), o the product of A's
         // off-diagonal parts; on it, where a = 0, b d + c (d^2 + o)
-        const float* diag = args.diag + static_cast<int64_t>(ti.g) * args.diag_ld;
         float* dout = args.diag_out + static_cast<int64_t>(ti.g) * args.diag_ld;
         __half* omat = static_cast<__half*>(args.out) + ti.g * args.out_stride;
         const int row0 = row - lane;
-        float di[4];
-#pragma unroll
-        for (int it4 = 0; it4 < 4; ++it4) {
-          const int pr = row0 + it4 * 8 + lane / 4;
-          di[it4] = pr < args.m ? diag[pr] : 0.0f;
-        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int col = col0 + c * 32;
@@ -680,18 +716,16 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           uint4 out[4];
           if (col < col_end) {
             stage_acc(taddr + c * 32);
-            float dj[8] = {};
-            if (pc < args.ld) {
-              Vec16<float>::load(diag + pc, dj);
-              Vec16<float>::load(diag + pc + 4, dj + 4);
-            }
+            float dj[8];
+            Vec16<float>::load(diag_cols + c * 32 + (lane % 4) * 8, dj);
+            Vec16<float>::load(diag_cols + c * 32 + (lane % 4) * 8 + 4, dj + 4);
 #pragma unroll
             for (int it4 = 0; it4 < 4; ++it4) {
               const int pr = row0 + it4 * 8 + lane / 4;
               float a[8], y[8];
               unpack_half8(src_hi[c & 1].v[it4], a);
               take_acc(it4, y);
-              const float d = di[it4];
+              const float d = drow[it4];
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 y[j] = args.cb * a[j] + args.cc * ((d + dj[j]) * a[j] + y[j]);
@@ -706,7 +740,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
           }
           fetch_ahead(c);
-          if (col < col_end && ti.m_blk != ti.n_blk) {
+          if (col < col_end && ti.m_blk != ti.n_blk / per_blk) {
             // the mirrored tile, transposed through the staging area in rows of
             // 72 bytes
             constexpr int pitch = 72;
@@ -734,28 +768,19 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       } else {
         // X' = a (hi + lo) + d hi + (B off its diagonal) hi, all times `scale`;
         // d is B's diagonal, of the row where B stands on the left
-        const float* diag = args.diag + static_cast<int64_t>(ti.g) * args.diag_ld;
         const int64_t src_base = ti.g * (static_cast<int64_t>(args.m) * args.ld);
         const bool last = args.out_lo == nullptr;
         const float inv = 1.0f / args.scale;
         const int row0 = row - lane;
-        float dr[4];
-#pragma unroll
-        for (int it4 = 0; it4 < 4; ++it4) {
-          const int pr = row0 + it4 * 8 + lane / 4;
-          dr[it4] = !args.diag_cols && pr < args.m ? diag[pr] : 0.0f;
-        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int col = col0 + c * 32;
           const int pc = col + (lane % 4) * 8;
           if (col < col_end) {
             stage_acc(taddr + c * 32);
-            float dc[8] = {};
-            if (args.diag_cols && pc < args.ld) {
-              Vec16<float>::load(diag + pc, dc);
-              Vec16<float>::load(diag + pc + 4, dc + 4);
-            }
+            float dc[8];
+            Vec16<float>::load(diag_cols + c * 32 + (lane % 4) * 8, dc);
+            Vec16<float>::load(diag_cols + c * 32 + (lane % 4) * 8 + 4, dc + 4);
 #pragma unroll
             for (int it4 = 0; it4 < 4; ++it4) {
               const int pr = row0 + it4 * 8 + lane / 4;
@@ -765,7 +790,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
               take_acc(it4, y);
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                y[j] = args.ca * (h[j] + l[j]) + (dr[it4] + dc[j]) * h[j] + y[j];
+                y[j] = args.ca * (h[j] + l[j]) + (drow[it4] + dc[j]) * h[j] + y[j];
               if (pr >= args.m || pc >= ld_end) continue;
               if (!last) {
                 const int64_t at = src_base + static_cast<int64_t>(pr) * args.ld + pc;
@@ -783,6 +808,12 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 for (int j = 0; j < 8; ++j) y[j] *= inv;
                 if (args.vec_ok) {
                   Vec16<bf16>::store(out, y);
+                } else if (args.n % 2 == 0) {
+#pragma unroll
+                  for (int j = 0; j < 8; j += 2)
+                    if (pc + j < col_end)
+                      *reinterpret_cast<__nv_bfloat162*>(out + j) =
+                          __floats2bfloat162_rn(y[j], y[j + 1]);
                 } else {
 #pragma unroll
                   for (int j = 0; j < 8; ++j)

@@ -71,12 +71,27 @@ bool make_map_16bit(CUtensorMap* map, bool fp16, const void* base, uint64_t inne
 // smaller box leaves room for seven stages of weights instead of five.
 enum MmRows { kMmRows128 = 128, kMmRows64 = 64 };
 
-// Columns of each of the equal tiles that n columns are cut into, at most 256,
-// in the MMA's steps of 32 (n = 1288: six tiles of 224, not five of 256 and
-// one of 8).
-inline int32_t mm_tile_width(int32_t n) {
-  const int32_t tiles = (n + 255) / 256;
+// Columns of a tile: n cut into equal tiles of at most 256, in the MMA's steps
+// of 32 (n = 1288: six tiles of 224, not five of 256 and one of 8).  Where
+// `bands` such rows of tiles leave pairs of CTAs idle, tiles are 128 or 64
+// wide.
+inline int32_t mm_tile_width(int32_t n, int64_t bands, int pairs) {
+  int32_t most = 256;
+  while (most > 64 && bands * ((n + most / 2 - 1) / (most / 2)) <= pairs) most /= 2;
+  const int32_t tiles = (n + most - 1) / most;
   return ((n + tiles - 1) / tiles + 31) / 32 * 32;
+}
+// The same for a symmetric product (kMmBatchSym) of `mats` matrices of side n,
+// whose tiles divide a block of 256; *tiles gets their number.
+inline int32_t mm_tile_width_sym(int32_t n, int64_t mats, int pairs, int64_t* tiles) {
+  const int64_t blocks = (n + 255) / 256;
+  auto count = [&](int32_t w) {
+    return mats * (256 / w * (blocks * (blocks - 1) / 2) + (n + w - 1) / w);
+  };
+  int32_t w = 256;
+  while (w > 64 && count(w / 2) <= pairs) w /= 2;
+  *tiles = count(w);
+  return w;
 }
 
 // Box rows of the A (or B) map of a layout: MN-major operands come in slices

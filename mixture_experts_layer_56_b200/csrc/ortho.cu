@@ -209,9 +209,12 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
                         tall ? mm_box_a(upd_layout) : mm_box_b(upd_layout));
   }
   if (!ok) return MOE_ERR_CUDA;
-  const int64_t mt = (L.m + 255) / 256, rt = (rows + 255) / 256, ct = (cols + 255) / 256;
-  const int64_t sym_tiles = mats * (mt * (mt + 1) / 2), upd_tiles = mats * rt * ct;
   const int most = sms / 2;
+  int64_t sym_tiles = 0;
+  const int32_t sym_tn = mm_tile_width_sym(L.m, mats, most, &sym_tiles);
+  const int64_t bands = static_cast<int64_t>(mats) * ((rows + 255) / 256);
+  const int32_t upd_tn = mm_tile_width(cols, bands, most);
+  const int64_t upd_tiles = bands * ((cols + upd_tn - 1) / upd_tn);
   const int sym_pairs = static_cast<int>(sym_tiles < most ? sym_tiles : most);
   const int upd_pairs = static_cast<int>(upd_tiles < most ? upd_tiles : most);
   for (int s = 0; s < steps; ++s) {
@@ -227,7 +230,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
     a.diag_ld = static_cast<int32_t>(L.ldm);
     // A = X X^T
     a.m = a.n = L.m;
-    a.tn = 256;  // square tiles: the symmetric products skip those above the diagonal
+    a.tn = sym_tn;
     a.k = tall ? rows : cols;
     a.out = ws + L.gram;
     a.ld = L.ldm;
@@ -246,7 +249,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
     const bool last = s == steps - 1;
     a.m = rows;
     a.n = cols;
-    a.tn = mm_tile_width(cols);
+    a.tn = upd_tn;
     a.src = ws + (cur ? L.hi1 : L.hi0);
     a.src_lo = ws + L.lo;
     a.diag = reinterpret_cast<const float*>(ws + L.dpoly);

@@ -102,7 +102,7 @@ int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const
   a.out = out;
   a.ld = n;
   a.status = static_cast<int32_t*>(ws);
-  a.tn = mm_tile_width(n);
+  a.tn = mm_tile_width(n, ragged_row_blocks(s), sms / 2);
   return launch_mm(layout, kMmRaggedM, kMmStoreBf16, box, ma, mb, a,
                    pairs_for(ragged_row_blocks(s) * ((n + a.tn - 1) / a.tn), sms), st);
 }
@@ -201,13 +201,14 @@ int moe_grouped_matmul_dw(const moe_grouped_shape_t* shape, const void* dY, cons
   a.groups = s.n_groups;
   a.m = s.n;
   a.n = s.k;
-  a.tn = mm_tile_width(s.k);
+  const int64_t bands = static_cast<int64_t>(s.n_groups) * ((s.n + 255) / 256);
+  a.tn = mm_tile_width(s.k, bands, sms / 2);
   a.out = dW;
   a.ld = s.k;
   a.out_stride = static_cast<int64_t>(s.n) * s.k;
   a.status = static_cast<int32_t*>(ws);
   const int epi = add ? kMmAddF32 : (f32_out ? kMmStoreF32 : kMmStoreBf16);
-  const int64_t tiles = static_cast<int64_t>(s.n_groups) * ((s.n + 255) / 256) * ((s.k + a.tn - 1) / a.tn);
+  const int64_t tiles = bands * ((s.k + a.tn - 1) / a.tn);
   return launch_mm(kMmTN, kMmRaggedK, epi, kMmRows128, ma, mb, a, pairs_for(tiles, sms), st);
 }
 

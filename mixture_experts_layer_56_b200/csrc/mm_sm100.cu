@@ -365,7 +365,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const bool mine = has_rows(ti, static_cast<int>(rank));
       // of an MN-major B the slices that the tile's width takes
       const bool two = !B_MN || ti.ncols > 128;
-      const uint32_t b_bytes = two ? B_BYTES : kSliceBytes;
+      const uint32_t b_bytes = B_MN ? (two ? B_BYTES : kSliceBytes)
+                                    : static_cast<uint32_t>(tn / 2) * (kKB * 2);
       const uint32_t bytes = (mine ? A_BYTES : 0) + b_bytes;
       const uint32_t pair_bytes = 2 * b_bytes + A_BYTES + (has_rows(ti, 1) ? A_BYTES : 0);
       const int za = RAG_M || RAG_K ? 0 : ti.g;

@@ -95,11 +95,13 @@ inline int32_t mm_tile_width_sym(int32_t n, int64_t mats, int pairs, int64_t* ti
 }
 
 // Box rows of the A (or B) map of a layout: MN-major operands come in slices
-// of 64 k rows.
+// of 64 k rows, a K-major B in a CTA's half of the tile's columns.
 inline uint32_t mm_box_a(int layout, int rows = kMmRows128) {
   return layout == kMmTN ? 64u : static_cast<uint32_t>(rows);
 }
-inline uint32_t mm_box_b(int layout) { return layout == kMmNT ? 128u : 64u; }
+inline uint32_t mm_box_b(int layout, int32_t tn) {
+  return layout == kMmNT ? static_cast<uint32_t>(tn / 2) : 64u;
+}
 
 // `pairs` CTA pairs compute the product.
 int launch_mm(int layout, int sched, int epi, int rows, const CUtensorMap& a, const CUtensorMap& b,

@@ -199,16 +199,6 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
   // operands of the three products (see mm_sm100.h)
   const int gram_layout = tall ? kMmTN : kMmNT;
   const int upd_layout = tall ? kMmNT : kMmNN;
-  CUtensorMap xg[2], xu[2], ga, ba;
-  bool ok = make_map_16bit(&ga, true, ws + L.gram, m64, m64, n64, L.ldm, gs, 128) &&
-            make_map_16bit(&ba, true, ws + L.poly, m64, m64, n64, L.ldm, gs, 128);
-  for (int i = 0; i < 2; ++i) {
-    void* x = ws + (i ? L.hi1 : L.hi0);
-    ok = ok && make_map_16bit(&xg[i], true, x, c64, r64, n64, L.ldx, xs, mm_box_a(gram_layout)) &&
-         make_map_16bit(&xu[i], true, x, c64, r64, n64, L.ldx, xs,
-                        tall ? mm_box_a(upd_layout) : mm_box_b(upd_layout));
-  }
-  if (!ok) return MOE_ERR_CUDA;
   const int most = sms / 2;
   int64_t sym_tiles = 0;
   const int32_t sym_tn = mm_tile_width_sym(L.m, mats, most, &sym_tiles);
@@ -217,6 +207,22 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
   const int64_t upd_tiles = bands * ((cols + upd_tn - 1) / upd_tn);
   const int sym_pairs = static_cast<int>(sym_tiles < most ? sym_tiles : most);
   const int upd_pairs = static_cast<int>(upd_tiles < most ? upd_tiles : most);
+  // each matrix as the A and as the B operand of what it enters; X twice, for
+  // the steps read and write it in turn
+  CUtensorMap xa[2], xb[2], xu[2], ga, gb, bu;
+  bool ok = make_map_16bit(&ga, true, ws + L.gram, m64, m64, n64, L.ldm, gs, mm_box_a(kMmNT)) &&
+            make_map_16bit(&gb, true, ws + L.gram, m64, m64, n64, L.ldm, gs,
+                           mm_box_b(kMmNT, sym_tn)) &&
+            make_map_16bit(&bu, true, ws + L.poly, m64, m64, n64, L.ldm, gs,
+                           tall ? mm_box_b(upd_layout, upd_tn) : mm_box_a(upd_layout));
+  for (int i = 0; i < 2; ++i) {
+    void* x = ws + (i ? L.hi1 : L.hi0);
+    ok = ok && make_map_16bit(&xa[i], true, x, c64, r64, n64, L.ldx, xs, mm_box_a(gram_layout)) &&
+         make_map_16bit(&xb[i], true, x, c64, r64, n64, L.ldx, xs, mm_box_b(gram_layout, sym_tn)) &&
+         make_map_16bit(&xu[i], true, x, c64, r64, n64, L.ldx, xs,
+                        tall ? mm_box_a(upd_layout) : mm_box_b(upd_layout, upd_tn));
+  }
+  if (!ok) return MOE_ERR_CUDA;
   for (int s = 0; s < steps; ++s) {
     const int cur = s & 1;
     MmArgs a{};
@@ -236,7 +242,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
     a.ld = L.ldm;
     a.out_stride = static_cast<int64_t>(gs);
     a.diag_out = reinterpret_cast<float*>(ws + L.dgram);
-    if (int e = launch_mm(gram_layout, kMmBatchSym, kMmGram, kMmRows128, xg[cur], xg[cur], a, sym_pairs, st))
+    if (int e = launch_mm(gram_layout, kMmBatchSym, kMmGram, kMmRows128, xa[cur], xb[cur], a, sym_pairs, st))
       return e;
     // B = b A + c A A
     a.k = L.m;
@@ -244,7 +250,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
     a.diag = reinterpret_cast<const float*>(ws + L.dgram);
     a.out = ws + L.poly;
     a.diag_out = reinterpret_cast<float*>(ws + L.dpoly);
-    if (int e = launch_mm(kMmNT, kMmBatchSym, kMmPoly, kMmRows128, ga, ga, a, sym_pairs, st)) return e;
+    if (int e = launch_mm(kMmNT, kMmBatchSym, kMmPoly, kMmRows128, ga, gb, a, sym_pairs, st)) return e;
     // X <- a X + B X, the last time as bf16 into O
     const bool last = s == steps - 1;
     a.m = rows;
@@ -265,7 +271,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
       a.out_stride = static_cast<int64_t>(xs);
       a.out_lo = ws + L.lo;  // each element is read and then written by one thread
     }
-    if (int e = launch_mm(upd_layout, kMmBatch, kMmUpdate, kMmRows128, tall ? xu[cur] : ba, tall ? ba : xu[cur],
+    if (int e = launch_mm(upd_layout, kMmBatch, kMmUpdate, kMmRows128, tall ? xu[cur] : bu, tall ? bu : xu[cur],
                           a, upd_pairs, st))
       return e;
   }

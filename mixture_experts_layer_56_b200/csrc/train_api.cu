@@ -89,9 +89,10 @@ int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const
   const int32_t n = dx ? s.k : s.n, k = dx ? s.n : s.k;  // of the product
   const uint64_t k64 = k, rows = s.rows, wn = s.n, wk = s.k;
   const int box = s.rows <= 64 ? kMmRows64 : kMmRows128;
+  const int32_t tn = mm_tile_width(n, ragged_row_blocks(s), sms / 2);
   CUtensorMap ma, mb;
   if (!make_map_16bit(&ma, false, in, k64, rows, 1, k64, rows * k64, mm_box_a(layout, box)) ||
-      !make_map_16bit(&mb, false, W, wk, wn, s.n_groups, wk, wn * wk, mm_box_b(layout)))
+      !make_map_16bit(&mb, false, W, wk, wn, s.n_groups, wk, wn * wk, mm_box_b(layout, tn)))
     return MOE_ERR_CUDA;
   MmArgs a{};
   a.offsets = offsets;
@@ -102,7 +103,7 @@ int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const
   a.out = out;
   a.ld = n;
   a.status = static_cast<int32_t*>(ws);
-  a.tn = mm_tile_width(n, ragged_row_blocks(s), sms / 2);
+  a.tn = tn;
   return launch_mm(layout, kMmRaggedM, kMmStoreBf16, box, ma, mb, a,
                    pairs_for(ragged_row_blocks(s) * ((n + a.tn - 1) / a.tn), sms), st);
 }
@@ -191,9 +192,11 @@ int moe_grouped_matmul_dw(const moe_grouped_shape_t* shape, const void* dY, cons
                               static_cast<const float*>(X), offsets, s.n_groups, s.rows, s.n, s.k,
                               static_cast<float*>(dW), add, sms, st);
   const uint64_t n = s.n, k = s.k, rows = s.rows;
+  const int64_t bands = static_cast<int64_t>(s.n_groups) * ((s.n + 255) / 256);
+  const int32_t tn = mm_tile_width(s.k, bands, sms / 2);
   CUtensorMap ma, mb;
   if (!make_map_16bit(&ma, false, dY, n, rows, 1, n, rows * n, mm_box_a(kMmTN)) ||
-      !make_map_16bit(&mb, false, X, k, rows, 1, k, rows * k, mm_box_b(kMmTN)))
+      !make_map_16bit(&mb, false, X, k, rows, 1, k, rows * k, mm_box_b(kMmTN, tn)))
     return MOE_ERR_CUDA;
   MmArgs a{};
   a.offsets = offsets;
@@ -201,8 +204,7 @@ int moe_grouped_matmul_dw(const moe_grouped_shape_t* shape, const void* dY, cons
   a.groups = s.n_groups;
   a.m = s.n;
   a.n = s.k;
-  const int64_t bands = static_cast<int64_t>(s.n_groups) * ((s.n + 255) / 256);
-  a.tn = mm_tile_width(s.k, bands, sms / 2);
+  a.tn = tn;
   a.out = dW;
   a.ld = s.k;
   a.out_stride = static_cast<int64_t>(s.n) * s.k;

@@ -269,7 +269,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
     } else {
       a.out = ws + (cur ? L.hi0 : L.hi1);
       a.out_stride = static_cast<int64_t>(xs);
-      a.out_lo = ws + L.lo;  // each element is read and then written by one thread
+      a.out_lo = ws + L.lo;  // each element is read and then written by one warp
     }
     if (int e = launch_mm(upd_layout, kMmBatch, kMmUpdate, kMmRows128, tall ? xu[cur] : bu, tall ? bu : xu[cur],
                           a, upd_pairs, st))

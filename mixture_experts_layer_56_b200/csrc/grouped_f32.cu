@@ -263,10 +263,12 @@ int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* o
     return nt * (dir == kGroupedDw ? static_cast<int64_t>(groups) * ((n + T - 1) / T)
                                    : (rows + T - 1) / T + some);
   };
-  // 128 x 128 tiles where they give every SM one and groups fill them (two
-  // blocks of them per SM, or one where the sums apart take the registers)
-  const bool fill = dir == kGroupedDw || rows >= 96 * some;
-  if (fill && tiles(128) >= sms)
+  // The tile size whose most loaded SM is done first: a 128 x 128 tile is four
+  // 64 x 64 ones, which take 1.45 times as long for the same work (8 x 1024 x
+  // 2048 x 1024: 49 against 34 TFLOP/s; 16 x 300 x 512 x 512: 105 against 93 us).
+  auto rounds = [&](int T) { return (tiles(T) + sms - 1) / sms; };
+  const bool fill = dir == kGroupedDw || rows >= 96 * some;  // groups fill the large ones
+  if (fill && 4.0 * rounds(128) <= 1.45 * rounds(64))
     return launch_tiles<8>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(128),
                            dir == kGroupedDw ? sms : 2 * sms, st);
   return launch_tiles<4>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(64),

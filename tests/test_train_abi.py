@@ -191,8 +191,11 @@ def test_orthogonalize_refuses_bad_pointers(lib):
 
 
 def test_workspaces_grow_with_their_shapes(lib):
-    sizes = [L.moe_orthogonalize_workspace_size(L.make_ortho_shape(n, 48, 80)) for n in (1, 2, 9)]
+    sizes = [L.moe_orthogonalize_workspace_size(L.make_ortho_shape(n, 148, 180)) for n in (1, 2, 9)]
     assert sizes[0] < sizes[1] < sizes[2] and all(x % 256 == 0 for x in sizes)
+    # matrices that stay on chip need the status word alone
+    assert [L.moe_orthogonalize_workspace_size(L.make_ortho_shape(n, *rc)) for n in (1, 9)
+            for rc in ((48, 80), (2048, 128))] == [256] * 4
     assert L.moe_layer_norm_workspace_size(L.make_norm_shape(0, 64)) == 0
     assert (L.moe_layer_norm_workspace_size(L.make_norm_shape(1, 64))
             < L.moe_layer_norm_workspace_size(L.make_norm_shape(4096, 64)))

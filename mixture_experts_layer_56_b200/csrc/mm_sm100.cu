@@ -3,6 +3,7 @@
 //
 //   forward          Y[r]  = X[r] W_g^T      NT, ragged rows
 //   input gradient   dX[r] = dY[r] W_g       NN, ragged rows
+//   (few rows)       the same, transposed    NT and TT, ragged columns
 //   weight gradient  dW_g  = dY_g^T X_g      TN, ragged reduction
 //   Newton-Schulz    X X^T, A A, B X         any, a batch of equal matrices
 //
@@ -50,11 +51,11 @@ constexpr int kWarpDiag = 128 * 4;  // a diagonal's values over an epilogue warp
 constexpr uint32_t kSliceBytes = 64 * kKB * 2;  // an MN-major 64-wide slice
 constexpr int kColChunk = 8;  // N tiles that a group's row blocks sweep together
 
-// Shared memory with AR rows of A in a stage.
-template <int AR>
+// Shared memory with BR rows of B per CTA in a stage.
+template <int BR>
 struct Stage {
-  static constexpr uint32_t kA = AR * kKB * 2;
-  static constexpr uint32_t kB = kHalf * kKB * 2;
+  static constexpr uint32_t kA = kHalf * kKB * 2;
+  static constexpr uint32_t kB = BR * kKB * 2;
   static constexpr uint32_t kBytes = kA + kB;
   // what 227 KB hold beside the epilogue's staging and 5 KB of barriers,
   // group tables and alignment
@@ -145,21 +146,22 @@ struct Tile {
   int ncols; // of the MMA
 };
 
-template <int LAYOUT, int SCHED, int EPI, bool FP16, int AR>
+template <int LAYOUT, int SCHED, int EPI, bool FP16, int BR>
 __global__ void __launch_bounds__(kThreads, 1)
 mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const MmArgs args) {
-  constexpr bool A_MN = LAYOUT == kMmTN;
-  constexpr bool B_MN = LAYOUT != kMmNT;
+  constexpr bool A_MN = LAYOUT == kMmTN || LAYOUT == kMmTT;
+  constexpr bool B_MN = LAYOUT == kMmNN || LAYOUT == kMmTN;
   constexpr bool RAG_M = SCHED == kMmRaggedM;
   constexpr bool RAG_K = SCHED == kMmRaggedK;
+  constexpr bool RAG_N = SCHED == kMmRaggedN;
   constexpr bool SYM = SCHED == kMmBatchSym;
-  constexpr uint32_t A_BYTES = Stage<AR>::kA;
-  constexpr uint32_t B_BYTES = Stage<AR>::kB;
-  constexpr uint32_t STAGE_BYTES = Stage<AR>::kBytes;
-  constexpr int STAGES = Stage<AR>::kCount;
+  constexpr uint32_t A_BYTES = Stage<BR>::kA;
+  constexpr uint32_t B_BYTES = Stage<BR>::kB;
+  constexpr uint32_t STAGE_BYTES = Stage<BR>::kBytes;
+  constexpr int STAGES = Stage<BR>::kCount;
   constexpr uint32_t TMEM_COLS = 2 * kTile;
-  static_assert(!A_MN || AR == 128, "an MN-major A comes in two slices");
+  static_assert(!B_MN || BR == 128, "an MN-major B comes in up to two slices");
   constexpr uint16_t kBoth = 0x3;
 
   extern __shared__ uint8_t smem_raw[];
@@ -218,7 +220,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   }
   pdl_wait();
   pdl_trigger();
-  if (RAG_M || RAG_K) {
+  if (RAG_M || RAG_K || RAG_N) {
     // Offsets are held to 0 <= first <= last <= rows, so that no value of
     // them reaches outside the operands.
     for (int g = tid; g < G; g += kThreads) {
@@ -226,7 +228,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const int b = min(max(args.offsets[g + 1], a), args.rows);
       grp_row0[g] = a;
       grp_rows[g] = b - a;
-      tile_start[g + 1] = ((b - a + kTile - 1) / kTile) * nt;
+      tile_start[g + 1] = RAG_N ? ((b - a + tn - 1) / tn) * ((args.m + kTile - 1) / kTile)
+                                : ((b - a + kTile - 1) / kTile) * nt;
     }
     __syncthreads();
     if (RAG_K) {
@@ -238,7 +241,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         grp_order[before] = static_cast<int16_t>(g);
       }
     }
-    if (RAG_M && warp == 0) {
+    if ((RAG_M || RAG_N) && warp == 0) {
       const int per = (G + 31) / 32;
       const int beg = min(lane * per, G);
       const int end = min(beg + per, G);
@@ -268,7 +271,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int per_blk = kTile / tn;
   const int per_group =
       SYM ? per_blk * (mt_fixed * (mt_fixed - 1) / 2) + nt : mt_fixed * nt;
-  const int total_tiles = RAG_M ? tile_start[G] : G * per_group;
+  const int total_tiles = RAG_M || RAG_N ? tile_start[G] : G * per_group;
 
   // position v of this pair's sequence cluster, cluster + nclusters, ...
   auto tile_of = [&](int v) {
@@ -282,7 +285,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const int here = min(nclusters, total_tiles - first);
       if (round & 1) t = first + here - 1 - (v - first);
     }
-    if (RAG_M) {
+    if (RAG_M || RAG_N) {
       int lo = 0, hi = G - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -292,15 +295,22 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       // the pairs in flight share a slice of the group's matrix in L2
       ti.g = lo;
       const int local = t - tile_start[lo];
-      const int mt = (tile_start[lo + 1] - tile_start[lo]) / nt;
-      const int cw = min(kColChunk, nt);
-      const int c = local / (cw * mt);
-      const int rem = local - c * cw * mt;
-      const int wc = min(cw, nt - c * cw);
-      ti.m_blk = rem / wc;
-      ti.n_blk = c * cw + (rem - ti.m_blk * wc);
       ti.row0 = grp_row0[lo];
       ti.rows = grp_rows[lo];
+      if (RAG_N) {
+        // the tiles of the same rows of the group's matrix side by side
+        const int blocks = (ti.rows + tn - 1) / tn;
+        ti.m_blk = local / blocks;
+        ti.n_blk = local - ti.m_blk * blocks;
+      } else {
+        const int mt = (tile_start[lo + 1] - tile_start[lo]) / nt;
+        const int cw = min(kColChunk, nt);
+        const int c = local / (cw * mt);
+        const int rem = local - c * cw * mt;
+        const int wc = min(cw, nt - c * cw);
+        ti.m_blk = rem / wc;
+        ti.n_blk = c * cw + (rem - ti.m_blk * wc);
+      }
     } else {
       ti.g = t / per_group;
       const int local = t - ti.g * per_group;
@@ -323,12 +333,12 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     ti.nkb = (ti.len + kKB - 1) / kKB;
     ti.col0 = ti.n_blk * tn;
     // the MMA's width: the last column tile's, in steps of 32
-    ti.ncols = min(tn, (args.n - ti.col0 + 31) & ~31);
+    ti.ncols = RAG_N ? tn : min(tn, (args.n - ti.col0 + 31) & ~31);
     return ti;
   };
   // whether CTA `r` of the pair has rows in the tile
   auto has_rows = [&](const Tile& ti, int r) {
-    return ti.m_blk * kTile + r * kHalf < (RAG_K ? args.m : ti.rows);
+    return ti.m_blk * kTile + r * kHalf < (RAG_K || RAG_N ? args.m : ti.rows);
   };
 
   // the same with every field known to be uniform across the warp
@@ -359,7 +369,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     for (int tile = cluster; tile < total_tiles && ok; tile += nclusters) {
       const Tile ti = uniform_tile(tile);
       const int m0 = ti.m_blk * kTile + static_cast<int>(rank) * kHalf + (RAG_M ? ti.row0 : 0);
-      const int n0 = ti.col0 + static_cast<int>(rank) * (ti.ncols / 2);
+      const int n0 = ti.col0 + static_cast<int>(rank) * (ti.ncols / 2) + (RAG_N ? ti.row0 : 0);
       // a CTA without rows leaves its part of A as it is: what the MMA makes
       // of it is not stored
       const bool mine = has_rows(ti, static_cast<int>(rank));
@@ -370,7 +380,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const uint32_t bytes = (mine ? A_BYTES : 0) + b_bytes;
       const uint32_t pair_bytes = 2 * b_bytes + A_BYTES + (has_rows(ti, 1) ? A_BYTES : 0);
       const int za = RAG_M || RAG_K ? 0 : ti.g;
-      const int zb = RAG_K ? 0 : ti.g;
+      const int zb = RAG_K || RAG_N ? 0 : ti.g;
       int k0 = RAG_K ? ti.row0 : 0;
       for (int kb = 0; kb < ti.nkb; ++kb, k0 += kKB) {
         ok = __all_sync(0xffffffffu,
@@ -612,7 +622,28 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                              static_cast<uint32_t>(acc * kTile + hcol * hw);
       const int64_t orow = RAG_M ? static_cast<int64_t>(ti.row0) + row : row;
       const int64_t obase = (RAG_M ? 0 : ti.g * args.out_stride) + orow * args.ld;
-      if (EPI == kMmStoreBf16) {
+      if (EPI == kMmStoreTBf16) {
+        // D's columns are the output's rows: 32 lanes hold 32 neighbours of
+        // each.  The halves of the warps take halves of the columns.
+        const int width = max(32, tn / 2);
+#pragma unroll 1
+        for (int c = hcol * width; c < min((hcol + 1) * width, tn); c += 32) {
+          const int left = ti.rows - ti.col0 - c;  // rows of the group from here
+          if (left <= 0) break;
+          float x[32];
+          tmem_ld32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                        static_cast<uint32_t>(acc * kTile + c),
+                    x);
+          tmem_ld_wait_regs(x);
+          if (row < args.m) {
+            bf16* out = static_cast<bf16*>(args.out) +
+                        (static_cast<int64_t>(ti.row0) + ti.col0 + c) * args.ld + row;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < left) out[static_cast<int64_t>(j) * args.ld] = __float2bfloat16_rn(x[j]);
+          }
+        }
+      } else if (EPI == kMmStoreBf16) {
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {  // a half is at most 128 wide
           const int col = col0 + c * 64;
@@ -857,22 +888,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-template <int LAYOUT, int SCHED, int EPI, bool FP16, int AR = 128>
+template <int LAYOUT, int SCHED, int EPI, bool FP16, int BR = 128>
 int launch_impl(const CUtensorMap& a, const CUtensorMap& b, const MmArgs& args, int pairs,
                 cudaStream_t st) {
   static std::atomic<uint64_t> optin{0};
-  auto kern = mm_pair_kernel<LAYOUT, SCHED, EPI, FP16, AR>;
-  constexpr int smem = Stage<AR>::kSmem;
+  auto kern = mm_pair_kernel<LAYOUT, SCHED, EPI, FP16, BR>;
+  constexpr int smem = Stage<BR>::kSmem;
   if (int rc = ensure_smem_optin(reinterpret_cast<const void*>(kern), smem, optin)) return rc;
   return launch_k(kern, dim3(2 * pairs), kThreads, smem, st, 2, a, b, args);
-}
-
-template <int LAYOUT>
-int launch_rows(int rows, const CUtensorMap& a, const CUtensorMap& b, const MmArgs& args, int pairs,
-                cudaStream_t st) {
-  if (rows == kMmRows64)
-    return launch_impl<LAYOUT, kMmRaggedM, kMmStoreBf16, false, 64>(a, b, args, pairs, st);
-  return launch_impl<LAYOUT, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
 }
 
 }  // namespace
@@ -891,12 +914,20 @@ bool make_map_16bit(CUtensorMap* map, bool fp16, const void* base, uint64_t inne
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launch_mm(int layout, int sched, int epi, int rows, const CUtensorMap& a, const CUtensorMap& b,
+int launch_mm(int layout, int sched, int epi, const CUtensorMap& a, const CUtensorMap& b,
               const MmArgs& args, int pairs, cudaStream_t st) {
   if (pairs <= 0) return MOE_OK;
   if (sched == kMmRaggedM && epi == kMmStoreBf16) {
-    if (layout == kMmNT) return launch_rows<kMmNT>(rows, a, b, args, pairs, st);
-    if (layout == kMmNN) return launch_rows<kMmNN>(rows, a, b, args, pairs, st);
+    if (layout == kMmNT) return launch_impl<kMmNT, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
+    if (layout == kMmNN) return launch_impl<kMmNN, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
+  }
+  if (sched == kMmRaggedN && epi == kMmStoreTBf16) {
+    if (args.tn > 64) {
+      if (layout == kMmNT) return launch_impl<kMmNT, kMmRaggedN, kMmStoreTBf16, false, 64>(a, b, args, pairs, st);
+      if (layout == kMmTT) return launch_impl<kMmTT, kMmRaggedN, kMmStoreTBf16, false, 64>(a, b, args, pairs, st);
+    }
+    if (layout == kMmNT) return launch_impl<kMmNT, kMmRaggedN, kMmStoreTBf16, false, 32>(a, b, args, pairs, st);
+    if (layout == kMmTT) return launch_impl<kMmTT, kMmRaggedN, kMmStoreTBf16, false, 32>(a, b, args, pairs, st);
   }
   if (sched == kMmRaggedK && layout == kMmTN) {
     if (epi == kMmStoreBf16) return launch_impl<kMmTN, kMmRaggedK, kMmStoreBf16, false>(a, b, args, pairs, st);

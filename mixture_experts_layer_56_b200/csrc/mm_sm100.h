@@ -16,11 +16,14 @@ enum MmLayout {
   kMmNT = 0,  // A [M, K], B [N, K]: both K-major
   kMmNN = 1,  // A [M, K] K-major, B [K, N] MN-major
   kMmTN = 2,  // A [K, M], B [K, N]: both MN-major
+  kMmTT = 3,  // A [K, M] MN-major, B [N, K] K-major
 };
 
 // What a tile's rows, columns and reduction come from.
 enum MmSched {
   kMmRaggedM = 0,  // rows offsets[g] .. offsets[g+1]-1 against matrix g
+  kMmRaggedN = 4,  // the same with the matrix as A and the rows as B: D is the
+                   // output's transpose
   kMmRaggedK = 1,  // the reduction runs over those rows; one output per group
   kMmBatch = 2,    // `groups` equal products
   kMmBatchSym = 3, // the same, D symmetric: only tiles on or below the diagonal
@@ -33,6 +36,7 @@ enum MmEpi {
   kMmGram = 3,     // Newton-Schulz: A = X X^T, diagonal apart
   kMmPoly = 4,     // Newton-Schulz: B = b A + c A A, diagonal apart
   kMmUpdate = 5,   // Newton-Schulz: X <- a X + B X
+  kMmStoreTBf16 = 6,  // D^T as bf16
 };
 
 constexpr int kMmMaxGroups = 256;
@@ -42,7 +46,7 @@ struct MmArgs {
   int32_t rows;            // ragged schedules: bound of the offsets
   int32_t groups;
   int32_t m;               // rows of D of one group (not kMmRaggedM)
-  int32_t n;               // columns of D
+  int32_t n;               // columns of D (not kMmRaggedN)
   int32_t tn;              // columns of a tile (mm_tile_width)
   int32_t k;               // reduction length (not kMmRaggedK)
   void* out;
@@ -66,10 +70,6 @@ struct MmArgs {
 // of a 16-bit type; strides in elements.
 bool make_map_16bit(CUtensorMap* map, bool fp16, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t depth, uint64_t ld, uint64_t stride, uint32_t box_rows);
-
-// Rows of A in a stage.  Where no group has more than 64 rows (decode), the
-// smaller box leaves room for seven stages of weights instead of five.
-enum MmRows { kMmRows128 = 128, kMmRows64 = 64 };
 
 // Columns of a tile: n cut into equal tiles of at most 256, in the MMA's steps
 // of 32 (n = 1288: six tiles of 224, not five of 256 and one of 8).  Where
@@ -95,16 +95,15 @@ inline int32_t mm_tile_width_sym(int32_t n, int64_t mats, int pairs, int64_t* ti
 }
 
 // Box rows of the A (or B) map of a layout: MN-major operands come in slices
-// of 64 k rows, a K-major B in a CTA's half of the tile's columns.
-inline uint32_t mm_box_a(int layout, int rows = kMmRows128) {
-  return layout == kMmTN ? 64u : static_cast<uint32_t>(rows);
-}
+// of 64 k rows, K-major ones in a CTA's 128 rows of A or its half of the
+// tile's columns.
+inline uint32_t mm_box_a(int layout) { return layout == kMmTN || layout == kMmTT ? 64u : 128u; }
 inline uint32_t mm_box_b(int layout, int32_t tn) {
-  return layout == kMmNT ? static_cast<uint32_t>(tn / 2) : 64u;
+  return layout == kMmNT || layout == kMmTT ? static_cast<uint32_t>(tn / 2) : 64u;
 }
 
 // `pairs` CTA pairs compute the product.
-int launch_mm(int layout, int sched, int epi, int rows, const CUtensorMap& a, const CUtensorMap& b,
+int launch_mm(int layout, int sched, int epi, const CUtensorMap& a, const CUtensorMap& b,
               const MmArgs& args, int pairs, cudaStream_t st);
 
 }  // namespace sm100

@@ -242,7 +242,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
     a.ld = L.ldm;
     a.out_stride = static_cast<int64_t>(gs);
     a.diag_out = reinterpret_cast<float*>(ws + L.dgram);
-    if (int e = launch_mm(gram_layout, kMmBatchSym, kMmGram, kMmRows128, xa[cur], xb[cur], a, sym_pairs, st))
+    if (int e = launch_mm(gram_layout, kMmBatchSym, kMmGram, xa[cur], xb[cur], a, sym_pairs, st))
       return e;
     // B = b A + c A A
     a.k = L.m;
@@ -250,7 +250,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
     a.diag = reinterpret_cast<const float*>(ws + L.dgram);
     a.out = ws + L.poly;
     a.diag_out = reinterpret_cast<float*>(ws + L.dpoly);
-    if (int e = launch_mm(kMmNT, kMmBatchSym, kMmPoly, kMmRows128, ga, gb, a, sym_pairs, st)) return e;
+    if (int e = launch_mm(kMmNT, kMmBatchSym, kMmPoly, ga, gb, a, sym_pairs, st)) return e;
     // X <- a X + B X, the last time as bf16 into O
     const bool last = s == steps - 1;
     a.m = rows;
@@ -271,7 +271,7 @@ int launch_orthogonalize(int dtype, const void* M, void* O, int mats, int rows, 
       a.out_stride = static_cast<int64_t>(xs);
       a.out_lo = ws + L.lo;  // each element is read and then written by one warp
     }
-    if (int e = launch_mm(upd_layout, kMmBatch, kMmUpdate, kMmRows128, tall ? xu[cur] : bu, tall ? bu : xu[cur],
+    if (int e = launch_mm(upd_layout, kMmBatch, kMmUpdate, tall ? xu[cur] : bu, tall ? bu : xu[cur],
                           a, upd_pairs, st))
       return e;
   }

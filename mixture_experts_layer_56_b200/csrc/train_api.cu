@@ -20,6 +20,7 @@ inline bool known_dtype(int32_t t) { return t == MOE_DTYPE_F32 || t == MOE_DTYPE
 
 constexpr size_t kStatusBytes = 256;  // the status word at the workspace's start
 constexpr int32_t kMaxSide = 1 << 24;
+constexpr int64_t kFewRows = 112;  // per group, on average
 
 int validate(const moe_grouped_shape_t* s) {
   if (!s) return MOE_ERR_NULLPTR;
@@ -85,26 +86,39 @@ int64_t ragged_row_blocks(const moe_grouped_shape_t& s) {
 int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const int32_t* offsets,
                     const void* W, void* out, void* ws, int sms, cudaStream_t st) {
   using namespace sm100;
-  const int layout = dx ? kMmNN : kMmNT;
   const int32_t n = dx ? s.k : s.n, k = dx ? s.n : s.k;  // of the product
   const uint64_t k64 = k, rows = s.rows, wn = s.n, wk = s.k;
-  const int box = s.rows <= 64 ? kMmRows64 : kMmRows128;
-  const int32_t tn = mm_tile_width(n, ragged_row_blocks(s), sms / 2);
-  CUtensorMap ma, mb;
-  if (!make_map_16bit(&ma, false, in, k64, rows, 1, k64, rows * k64, mm_box_a(layout, box)) ||
-      !make_map_16bit(&mb, false, W, wk, wn, s.n_groups, wk, wn * wk, mm_box_b(layout, tn)))
-    return MOE_ERR_CUDA;
   MmArgs a{};
   a.offsets = offsets;
   a.rows = static_cast<int32_t>(s.rows);
   a.groups = s.n_groups;
-  a.n = n;
   a.k = k;
   a.out = out;
   a.ld = n;
   a.status = static_cast<int32_t*>(ws);
-  a.tn = tn;
-  return launch_mm(layout, kMmRaggedM, kMmStoreBf16, box, ma, mb, a,
+  CUtensorMap ma, mb;
+  if (s.rows < kFewRows * s.n_groups) {
+    // Few rows per group: the weights' stream is what bounds the product, and
+    // tiles of 256 rows would be mostly empty and keep the tensor cores busy
+    // longer than the stream takes.  The groups' matrices take the rows' place:
+    // D is 256 output columns by 32 to 128 rows.
+    a.m = n;
+    a.tn = s.rows <= 32 ? 32 : s.rows <= 48ll * s.n_groups ? 64 : 128;
+    const int layout = dx ? kMmTT : kMmNT;
+    if (!make_map_16bit(&ma, false, W, wk, wn, s.n_groups, wk, wn * wk, mm_box_a(layout)) ||
+        !make_map_16bit(&mb, false, in, k64, rows, 1, k64, rows * k64, mm_box_b(layout, a.tn)))
+      return MOE_ERR_CUDA;
+    const int64_t blocks = s.rows / a.tn + (s.rows < s.n_groups ? s.rows : s.n_groups);
+    return launch_mm(layout, kMmRaggedN, kMmStoreTBf16, ma, mb, a,
+                     pairs_for(blocks * ((n + 255) / 256), sms), st);
+  }
+  const int layout = dx ? kMmNN : kMmNT;
+  a.n = n;
+  a.tn = mm_tile_width(n, ragged_row_blocks(s), sms / 2);
+  if (!make_map_16bit(&ma, false, in, k64, rows, 1, k64, rows * k64, mm_box_a(layout)) ||
+      !make_map_16bit(&mb, false, W, wk, wn, s.n_groups, wk, wn * wk, mm_box_b(layout, a.tn)))
+    return MOE_ERR_CUDA;
+  return launch_mm(layout, kMmRaggedM, kMmStoreBf16, ma, mb, a,
                    pairs_for(ragged_row_blocks(s) * ((n + a.tn - 1) / a.tn), sms), st);
 }
 
@@ -211,7 +225,7 @@ int moe_grouped_matmul_dw(const moe_grouped_shape_t* shape, const void* dY, cons
   a.status = static_cast<int32_t*>(ws);
   const int epi = add ? kMmAddF32 : (f32_out ? kMmStoreF32 : kMmStoreBf16);
   const int64_t tiles = bands * ((s.k + a.tn - 1) / a.tn);
-  return launch_mm(kMmTN, kMmRaggedK, epi, kMmRows128, ma, mb, a, pairs_for(tiles, sms), st);
+  return launch_mm(kMmTN, kMmRaggedK, epi, ma, mb, a, pairs_for(tiles, sms), st);
 }
 
 int moe_swiglu(const moe_swiglu_shape_t* shape, const void* gu, void* a, moe_stream_t stream) {

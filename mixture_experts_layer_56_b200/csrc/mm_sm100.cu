@@ -149,7 +149,7 @@ struct Tile {
 template <int LAYOUT, int SCHED, int EPI, bool FP16, int BR>
 __global__ void __launch_bounds__(kThreads, 1)
 mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const MmArgs args) {
+               const __grid_constant__ CUtensorMap tmTail, const MmArgs args) {
   constexpr bool A_MN = LAYOUT == kMmTN || LAYOUT == kMmTT;
   constexpr bool B_MN = LAYOUT == kMmNN || LAYOUT == kMmTN;
   constexpr bool RAG_M = SCHED == kMmRaggedM;
@@ -291,26 +291,22 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const int mid = (lo + hi + 1) >> 1;
         if (tile_start[mid] <= t) lo = mid; else hi = mid - 1;
       }
-      // a group's row blocks sweep kColChunk column tiles together, so that
-      // the pairs in flight share a slice of the group's matrix in L2
       ti.g = lo;
       const int local = t - tile_start[lo];
       ti.row0 = grp_row0[lo];
       ti.rows = grp_rows[lo];
-      if (RAG_N) {
-        // the tiles of the same rows of the group's matrix side by side
-        const int blocks = (ti.rows + tn - 1) / tn;
-        ti.m_blk = local / blocks;
-        ti.n_blk = local - ti.m_blk * blocks;
-      } else {
-        const int mt = (tile_start[lo + 1] - tile_start[lo]) / nt;
-        const int cw = min(kColChunk, nt);
-        const int c = local / (cw * mt);
-        const int rem = local - c * cw * mt;
-        const int wc = min(cw, nt - c * cw);
-        ti.m_blk = rem / wc;
-        ti.n_blk = c * cw + (rem - ti.m_blk * wc);
-      }
+      // the row blocks sweep kColChunk tiles along the matrix together, so that
+      // the pairs in flight share a slice of the group's matrix in L2
+      const int along = RAG_N ? (args.m + kTile - 1) / kTile : nt;
+      const int blocks = (tile_start[lo + 1] - tile_start[lo]) / along;
+      const int cw = min(kColChunk, along);
+      const int c = local / (cw * blocks);
+      const int rem = local - c * cw * blocks;
+      const int wc = min(cw, along - c * cw);
+      const int block = rem / wc;
+      const int at = c * cw + (rem - block * wc);
+      ti.m_blk = RAG_N ? at : block;
+      ti.n_blk = RAG_N ? block : at;
     } else {
       ti.g = t / per_group;
       const int local = t - ti.g * per_group;
@@ -332,8 +328,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     ti.len = RAG_K ? ti.rows : args.k;
     ti.nkb = (ti.len + kKB - 1) / kKB;
     ti.col0 = ti.n_blk * tn;
-    // the MMA's width: the last column tile's, in steps of 32
-    ti.ncols = RAG_N ? tn : min(tn, (args.n - ti.col0 + 31) & ~31);
+    // the MMA's width: the last column tile's, in steps of 32 (what makes a
+    // group's last rows cheaper as columns than in a tile of 256 rows)
+    ti.ncols = min(tn, ((RAG_N ? ti.rows : args.n) - ti.col0 + 31) & ~31);
     return ti;
   };
   // whether CTA `r` of the pair has rows in the tile
@@ -375,8 +372,12 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const bool mine = has_rows(ti, static_cast<int>(rank));
       // of an MN-major B the slices that the tile's width takes
       const bool two = !B_MN || ti.ncols > 128;
-      const uint32_t b_bytes = B_MN ? (two ? B_BYTES : kSliceBytes)
-                                    : static_cast<uint32_t>(tn / 2) * (kKB * 2);
+      // of a ragged group's last rows boxes of 32
+      const bool tail = RAG_N && BR == 128 && ti.ncols < tn;
+      const int boxes = tail ? (ti.ncols + 63) / 64 : 0;
+      const uint32_t b_bytes = B_MN   ? (two ? B_BYTES : kSliceBytes)
+                               : tail ? static_cast<uint32_t>(boxes) * (32 * kKB * 2)
+                                      : static_cast<uint32_t>(tn / 2) * (kKB * 2);
       const uint32_t bytes = (mine ? A_BYTES : 0) + b_bytes;
       const uint32_t pair_bytes = 2 * b_bytes + A_BYTES + (has_rows(ti, 1) ? A_BYTES : 0);
       const int za = RAG_M || RAG_K ? 0 : ti.g;
@@ -408,6 +409,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           if (B_MN) {
             tma_load_3d_pair(sb, &tmB, fb, n0, k0, zb);
             if (two) tma_load_3d_pair(sb + kSliceBytes, &tmB, fb, n0 + 64, k0, zb);
+          } else if (tail) {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_3d_pair(sb + i * (32 * kKB * 2), &tmTail, fb, k0, n0 + i * 32, zb);
           } else {
             tma_load_3d_pair(sb, &tmB, fb, k0, n0, zb);
           }
@@ -635,12 +639,28 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         static_cast<uint32_t>(acc * kTile + c),
                     x);
           tmem_ld_wait_regs(x);
-          if (row < args.m) {
-            bf16* out = static_cast<bf16*>(args.out) +
-                        (static_cast<int64_t>(ti.row0) + ti.col0 + c) * args.ld + row;
+          bf16* out = static_cast<bf16*>(args.out) +
+                      (static_cast<int64_t>(ti.row0) + ti.col0 + c) * args.ld + (row - lane);
+          if (left < 8) {
+            if (row < args.m) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (j < left) out[static_cast<int64_t>(j) * args.ld + lane] = __float2bfloat16_rn(x[j]);
+            }
+          } else {
+            // through the staging area, to 16-byte pieces of the output's rows
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (j < left) out[static_cast<int64_t>(j) * args.ld] = __float2bfloat16_rn(x[j]);
+              reinterpret_cast<bf16*>(stage + j * kStagePitch)[lane] = __float2bfloat16_rn(x[j]);
+            __syncwarp();
+#pragma unroll
+            for (int it4 = 0; it4 < 4; ++it4) {
+              const int j = it4 * 8 + lane / 4, piece = lane % 4;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + j * kStagePitch + piece * 16);
+              if (j < left && row - lane + piece * 8 < args.m)
+                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(j) * args.ld + piece * 8) = v;
+            }
+            __syncwarp();
           }
         }
       } else if (EPI == kMmStoreBf16) {
@@ -890,12 +910,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 template <int LAYOUT, int SCHED, int EPI, bool FP16, int BR = 128>
 int launch_impl(const CUtensorMap& a, const CUtensorMap& b, const MmArgs& args, int pairs,
-                cudaStream_t st) {
+                cudaStream_t st, const CUtensorMap* tail = nullptr) {
   static std::atomic<uint64_t> optin{0};
   auto kern = mm_pair_kernel<LAYOUT, SCHED, EPI, FP16, BR>;
   constexpr int smem = Stage<BR>::kSmem;
   if (int rc = ensure_smem_optin(reinterpret_cast<const void*>(kern), smem, optin)) return rc;
-  return launch_k(kern, dim3(2 * pairs), kThreads, smem, st, 2, a, b, args);
+  return launch_k(kern, dim3(2 * pairs), kThreads, smem, st, 2, a, b, tail ? *tail : b, args);
 }
 
 }  // namespace
@@ -915,13 +935,18 @@ bool make_map_16bit(CUtensorMap* map, bool fp16, const void* base, uint64_t inne
 }
 
 int launch_mm(int layout, int sched, int epi, const CUtensorMap& a, const CUtensorMap& b,
-              const MmArgs& args, int pairs, cudaStream_t st) {
+              const MmArgs& args, int pairs, cudaStream_t st, const CUtensorMap* tail) {
   if (pairs <= 0) return MOE_OK;
   if (sched == kMmRaggedM && epi == kMmStoreBf16) {
     if (layout == kMmNT) return launch_impl<kMmNT, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
     if (layout == kMmNN) return launch_impl<kMmNN, kMmRaggedM, kMmStoreBf16, false>(a, b, args, pairs, st);
   }
   if (sched == kMmRaggedN && epi == kMmStoreTBf16) {
+    if (args.tn > 128) {
+      if (!tail) return MOE_ERR_SHAPE;
+      if (layout == kMmNT) return launch_impl<kMmNT, kMmRaggedN, kMmStoreTBf16, false>(a, b, args, pairs, st, tail);
+      if (layout == kMmTT) return launch_impl<kMmTT, kMmRaggedN, kMmStoreTBf16, false>(a, b, args, pairs, st, tail);
+    }
     if (args.tn > 64) {
       if (layout == kMmNT) return launch_impl<kMmNT, kMmRaggedN, kMmStoreTBf16, false, 64>(a, b, args, pairs, st);
       if (layout == kMmTT) return launch_impl<kMmTT, kMmRaggedN, kMmStoreTBf16, false, 64>(a, b, args, pairs, st);

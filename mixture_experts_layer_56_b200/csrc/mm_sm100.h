@@ -102,9 +102,10 @@ inline uint32_t mm_box_b(int layout, int32_t tn) {
   return layout == kMmNT || layout == kMmTT ? static_cast<uint32_t>(tn / 2) : 64u;
 }
 
-// `pairs` CTA pairs compute the product.
+// `pairs` CTA pairs compute the product.  kMmRaggedN with tn = 256 takes a
+// second map of B, with a box of 32 rows, for the groups' last ones.
 int launch_mm(int layout, int sched, int epi, const CUtensorMap& a, const CUtensorMap& b,
-              const MmArgs& args, int pairs, cudaStream_t st);
+              const MmArgs& args, int pairs, cudaStream_t st, const CUtensorMap* tail = nullptr);
 
 }  // namespace sm100
 }  // namespace moe

@@ -20,7 +20,9 @@ inline bool known_dtype(int32_t t) { return t == MOE_DTYPE_F32 || t == MOE_DTYPE
 
 constexpr size_t kStatusBytes = 256;  // the status word at the workspace's start
 constexpr int32_t kMaxSide = 1 << 24;
-constexpr int64_t kFewRows = 112;  // per group, on average
+// Rows per group, on average, below which the products take the matrix's rows
+// as the tile's: see run_ragged_rows.
+constexpr int64_t kFewRows = 512;
 
 int validate(const moe_grouped_shape_t* s) {
   if (!s) return MOE_ERR_NULLPTR;
@@ -83,11 +85,21 @@ int64_t ragged_row_blocks(const moe_grouped_shape_t& s) {
 }
 
 // The bf16 products of ragged rows: forward (in = X) and dX (in = dY).
+//
+// Two ways round.  With the groups' rows as the tile's 256 rows, a group's last
+// tile costs a whole one, and where groups have few rows every tile is mostly
+// empty and keeps the tensor cores busy for longer than the weights' stream
+// takes.  With the matrix's rows in their place the groups' rows are columns,
+// which come in steps of 32: 64 groups of 2816 x 2048 with 12 rows each on
+// average take 116 us (0.98 of the HBM rate) for 146, with 96 rows 128 for 151,
+// with 200 rows 170 for 186.  From some 500 rows on there is nothing between
+// them but the output's transposition (16 groups of 4096 rows: 375 for 372 us).
 int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const int32_t* offsets,
                     const void* W, void* out, void* ws, int sms, cudaStream_t st) {
   using namespace sm100;
   const int32_t n = dx ? s.k : s.n, k = dx ? s.n : s.k;  // of the product
   const uint64_t k64 = k, rows = s.rows, wn = s.n, wk = s.k;
+  const bool swap = s.rows < kFewRows * s.n_groups;
   MmArgs a{};
   a.offsets = offsets;
   a.rows = static_cast<int32_t>(s.rows);
@@ -96,21 +108,18 @@ int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const
   a.out = out;
   a.ld = n;
   a.status = static_cast<int32_t*>(ws);
-  CUtensorMap ma, mb;
-  if (s.rows < kFewRows * s.n_groups) {
-    // Few rows per group: the weights' stream is what bounds the product, and
-    // tiles of 256 rows would be mostly empty and keep the tensor cores busy
-    // longer than the stream takes.  The groups' matrices take the rows' place:
-    // D is 256 output columns by 32 to 128 rows.
+  CUtensorMap ma, mb, tail;
+  if (swap) {
     a.m = n;
-    a.tn = s.rows <= 32 ? 32 : s.rows <= 48ll * s.n_groups ? 64 : 128;
+    a.tn = s.rows <= 32 ? 32 : s.rows <= 48ll * s.n_groups ? 64 : s.rows <= 112ll * s.n_groups ? 128 : 256;
     const int layout = dx ? kMmTT : kMmNT;
     if (!make_map_16bit(&ma, false, W, wk, wn, s.n_groups, wk, wn * wk, mm_box_a(layout)) ||
-        !make_map_16bit(&mb, false, in, k64, rows, 1, k64, rows * k64, mm_box_b(layout, a.tn)))
+        !make_map_16bit(&mb, false, in, k64, rows, 1, k64, rows * k64, mm_box_b(layout, a.tn)) ||
+        (a.tn == 256 && !make_map_16bit(&tail, false, in, k64, rows, 1, k64, rows * k64, 32)))
       return MOE_ERR_CUDA;
     const int64_t blocks = s.rows / a.tn + (s.rows < s.n_groups ? s.rows : s.n_groups);
     return launch_mm(layout, kMmRaggedN, kMmStoreTBf16, ma, mb, a,
-                     pairs_for(blocks * ((n + 255) / 256), sms), st);
+                     pairs_for(blocks * ((n + 255) / 256), sms), st, &tail);
   }
   const int layout = dx ? kMmNN : kMmNT;
   a.n = n;

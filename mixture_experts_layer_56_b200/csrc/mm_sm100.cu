@@ -22,8 +22,9 @@
 // Ragged rows need no masking: a tile may run past its group's last row, and
 // the rows it computes there are not stored.  A ragged reduction does: the
 // last k-block of a group holds the first rows of the next one (or rows that
-// nobody owns, which may hold NaN).  Warp 3 of each CTA zeroes those rows of
-// both operands in shared memory before the MMAs may read them.
+// nobody owns, which may hold NaN).  MMA steps of 16 that hold none of the
+// group's rows are not issued, and warp 3 of each CTA zeroes the rest of the
+// last one in both operands in shared memory before the MMAs may read it.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -64,26 +65,26 @@ struct Stage {
   static_assert(kCount >= 4 && kCount <= 16, "the issued-stage masks hold 32");
 };
 
-// Rows of 32 lanes (lane r holds row r, NV 16-byte pieces) written to global
-// memory as whole row segments through the warp's staging area.  `dst` is the
-// lane's row start (nullptr: not written) and `pieces` how many of the NV
-// pieces lie inside the matrix.
+// 32 rows (lane r holds row r, NV 16-byte pieces) written to global memory as
+// whole row segments through the warp's staging area: `dst` is where row 0
+// goes, `pitch` the bytes between rows; of the rows `rows` are written, and of
+// the pieces those below `pieces` (the others lie outside the matrix).
 template <int NV, typename Put>
-__device__ __forceinline__ void store_rows(uint8_t* stage, const uint4* v, uint8_t* dst, int pieces,
-                                           int lane, Put put) {
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint4* v, void* dst, int64_t pitch,
+                                           int rows, int pieces, int lane, Put put) {
   constexpr int RPI = 32 / NV;
 #pragma unroll
   for (int c = 0; c < NV; ++c)
     *reinterpret_cast<uint4*>(stage + lane * kStagePitch + c * 16) = v[c];
   __syncwarp();
+  const int c = lane % NV, r0 = lane / NV;
+  uint8_t* at = static_cast<uint8_t*>(dst) + r0 * pitch + c * 16;
+  if (c >= pieces) rows = 0;
 #pragma unroll
   for (int it = 0; it < NV; ++it) {
-    const int row = it * RPI + lane / NV;
-    const int c = lane % NV;
-    uint8_t* rdst = reinterpret_cast<uint8_t*>(
-        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
-    const uint4 x = *reinterpret_cast<const uint4*>(stage + row * kStagePitch + c * 16);
-    if (rdst != nullptr && c < pieces) put(reinterpret_cast<uint4*>(rdst + c * 16), x);
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + (it * RPI + r0) * kStagePitch + c * 16);
+    if (it * RPI + r0 < rows) put(reinterpret_cast<uint4*>(at), x);
+    at += RPI * pitch;
   }
   __syncwarp();
 }
@@ -391,7 +392,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const uint32_t sb = sa + A_BYTES;
         // a ragged group's last, partial k-block lands on this CTA's own
         // barrier, where warp 3 takes it over
-        const bool partial = RAG_K && kb == ti.nkb - 1 && (ti.rows & (kKB - 1)) != 0;
+        const bool partial = RAG_K && kb == ti.nkb - 1 && (ti.rows & 15) != 0;
         const uint32_t fb = partial || leader ? (partial ? land_bar(stage) : full_bar(stage))
                                               : map_to_cta(full_bar(stage), 0);
         if (elect_lane()) {
@@ -498,14 +499,15 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     int done = 0;         // stage of the next tile's first k-block
     for (int tile = cluster; tile < total_tiles; tile += nclusters) {
       const Tile ti = tile_of(tile);
-      const int rem = ti.rows & (kKB - 1);
-      if (rem != 0) {
+      if ((ti.rows & 15) != 0) {
+        const int rem = ti.rows & (kKB - 1);
         const int s = (done + ti.nkb - 1) % STAGES;
         if (!wait_bounded(land_bar(s), (parity >> s) & 1u, abort_p, args.status)) break;
         parity ^= 1u << s;
         uint8_t* base = smem + s * STAGE_BYTES;
-        // rows rem..63 are the tail of each of the four 64-wide slices
-        for (int o = rem * 128 + lane * 16; o < static_cast<int>(kSliceBytes); o += 512) {
+        // the rows from rem to the end of their step of 16 (the steps behind it
+        // are not issued), in each of the four 64-wide slices
+        for (int o = rem * 128 + lane * 16; o < ((rem + 15) & ~15) * 128; o += 512) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             *reinterpret_cast<uint4*>(base + c * kSliceBytes + o) = make_uint4(0, 0, 0, 0);
@@ -625,7 +627,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(acc * kTile + hcol * hw);
       const int64_t orow = RAG_M ? static_cast<int64_t>(ti.row0) + row : row;
-      const int64_t obase = (RAG_M ? 0 : ti.g * args.out_stride) + orow * args.ld;
+      // of this warp's 32 rows: where the first goes, and how many there are
+      const int64_t obase = (RAG_M ? 0 : ti.g * args.out_stride) + (orow - lane) * args.ld;
+      const int warp_rows = (RAG_K ? args.m : ti.rows) - (row - lane);
       if (EPI == kMmStoreTBf16) {
         // D's columns are the output's rows: 32 lanes hold 32 neighbours of
         // each.  The halves of the warps take halves of the columns.
@@ -683,8 +687,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           for (int i = 0; i < 8; ++i)
             Vec16<bf16>::store(reinterpret_cast<bf16*>(&v[i]), x + i * 8);
           bf16* out = static_cast<bf16*>(args.out) + obase + col;
-          store_rows<8>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
-                        (col_end - col) / 8, lane, PutPlain{});
+          store_rows<8>(stage, v, out, args.ld * 2, warp_rows, (col_end - col) / 8, lane, PutPlain{});
         }
       } else if (EPI == kMmStoreF32 || EPI == kMmAddF32) {
         if (!(EPI == kMmAddF32 && empty)) {
@@ -701,12 +704,11 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
               for (int i = 0; i < 32; ++i) x[i] = 0.0f;
             }
             float* out = static_cast<float*>(args.out) + obase + col;
-            uint8_t* dst = live ? reinterpret_cast<uint8_t*>(out) : nullptr;
             const uint4* v = reinterpret_cast<const uint4*>(x);
             if (EPI == kMmAddF32)
-              store_rows<8>(stage, v, dst, (col_end - col) / 4, lane, PutAddF32{});
+              store_rows<8>(stage, v, out, args.ld * 4, warp_rows, (col_end - col) / 4, lane, PutAddF32{});
             else
-              store_rows<8>(stage, v, dst, (col_end - col) / 4, lane, PutPlain{});
+              store_rows<8>(stage, v, out, args.ld * 4, warp_rows, (col_end - col) / 4, lane, PutPlain{});
           }
         }
       } else if (EPI == kMmGram) {
@@ -733,9 +735,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           uint4 v[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = pack_half8(x + i * 8);
-          __half* out = omat + static_cast<int64_t>(row) * args.ld + col;
-          store_rows<4>(stage, v, live ? reinterpret_cast<uint8_t*>(out) : nullptr,
-                        (ld_end - col) / 8, lane, PutPlain{});
+          __half* out = omat + static_cast<int64_t>(row - lane) * args.ld + col;
+          store_rows<4>(stage, v, out, args.ld * 2, warp_rows, (ld_end - col) / 8, lane, PutPlain{});
           if (SYM && ti.m_blk != ti.n_blk / per_blk) {
             // the mirrored tile: lane r writes column r of the staging area,
             // whose rows go out in 16-byte pieces

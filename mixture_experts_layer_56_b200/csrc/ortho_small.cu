@@ -67,8 +67,9 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
-__device__ __forceinline__ void fence_async_all() {
-  asm volatile("fence.proxy.async;" ::: "memory");
+// orders this thread's writes to any CTA's shared memory before the MMAs' reads
+__device__ __forceinline__ void fence_async_cluster() {
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
 }
 
 // byte offset of 16-byte piece `ch` (0..7) of row i in a swizzled 128-row tile
@@ -228,7 +229,7 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
   for (int step = 0; step < steps; ++step) {
     const float ca = coef.v[3 * step], cb = coef.v[3 * step + 1], cc = coef.v[3 * step + 2];
     // ---- 1. this CTA's part of X X^T ----------------------------------------
-    fence_async_all();  // hi was written by ordinary stores
+    fence_async_shared();  // hi was written by ordinary stores
     tc_fence_before();
     __syncthreads();
     if (tid == 0) {
@@ -268,7 +269,7 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
           *reinterpret_cast<uint4*>(sq + (col >> 6) * kSmSlice + tile_at(r, (col >> 3) & 7)) = w;
         }
       }
-      fence_async_all();
+      fence_async_shared();
       tc_fence_before();
       __syncthreads();
     } else {
@@ -327,12 +328,12 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
               st_cluster_f32(map_to_cta(smem_addr(&da[i]), static_cast<uint32_t>(p)), diag);
         }
       }
-      fence_async_all();
+      fence_async_cluster();
       cluster_sync_all();
     }
     // ---- 3. B = b A + c A A -------------------------------------------------
     if (tid == 0) {
-      fence_async_all();
+      fence_async_cluster();
       tc_fence_after();
       constexpr uint32_t idesc = idesc_16bit_f32(128, 128, true, false, false);
 #pragma unroll
@@ -378,7 +379,7 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
         *at = w;
       }
     }
-    fence_async_all();
+    fence_async_shared();
     tc_fence_before();
     __syncthreads();
     // ---- 4. X <- a X + B X --------------------------------------------------

@@ -282,16 +282,18 @@ int moe_expert_balance(const moe_shape_t* shape, const void* u, const void* E,
  * allocation, bitwise reproducible, capturable.  An output overlaps no input
  * unless its function says so.  A call that takes `ws` writes there: calls
  * that may run at the same time, replays of captured ones among them, need a
- * workspace each.
+ * workspace each.  Nothing in it has to be set before a call; but a workspace
+ * that moe_read_status is to be asked about (those of the grouped products and
+ * of moe_orthogonalize) has its first 4 bytes zeroed once.
  * ------------------------------------------------------------------------- */
 
 /* Ragged groups of rows, each with its own matrix: group g owns the rows
    offsets[g] .. offsets[g+1]-1 (device int32 [n_groups + 1], as moe_dispatch
    writes them) and W_g, row-major [n, k] in W [n_groups, n, k].  Groups may be
-   empty.  Offsets are expected non-decreasing in [0, rows]; a start is clamped
-   to that range and an end to [its start, rows], so that no offsets reach
-   outside the tensors.  Rows that no group owns are not read and not
-   written.
+   empty.  Offsets outside [0, rows] count as the nearer bound, and one below
+   an offset before it as that one: no offsets reach outside the tensors or
+   give a row to two groups.  Rows that no group owns are not written, and
+   nothing depends on them.
    Limits: 1 <= n_groups <= 256, 0 <= rows <= 2^31 - 512, 1 <= n, k <= 2^24;
    bf16: n and k multiples of 8; fp32 runs on the CUDA cores.  The products'
    64 x 64 output tiles must number fewer than 2^31, and the tensors be smaller
@@ -382,7 +384,10 @@ int moe_layer_norm_backward(const moe_norm_shape_t* shape, const void* dy, const
    returns; NULL means 3.4445, -4.7750, 2.0315 in each.  O [n_mats, rows,
    cols] is bfloat16, whatever the dtype of M.  The products run on the tensor
    cores with fp16 operands beside a 22-bit X, which needs the coefficients to
-   keep the singular values of every step's X below about 100.  A matrix of
+   keep the singular values of every step's X below about 10 (the defaults keep
+   them below 1.25), and O's error relative to its norm is about 2e-3, bf16's
+   own rounding among it.  Entries of X below about 2^-24 / sqrt(max(rows,
+   cols)) are lost, as in matrices whose norm is far below the 1e-7.  A matrix of
    zeros gives zeros; one with an infinity or NaN gives NaN, the others of the
    stack are untouched by it.  M's tensor may have any 1 <= rows, cols <=
    65536; n_mats <= 65535; 1 <= steps <= 16. */

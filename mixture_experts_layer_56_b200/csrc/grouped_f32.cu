@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "group_spans.cuh"
 #include "train_kernels.h"
 
 namespace moe {
@@ -120,13 +121,14 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
   const int N = FWD ? n : k;
   const int nt = (N + T - 1) / T;
   const int mt_dw = (n + T - 1) / T;
+  group_spans(offsets, groups, rows, tile_start, tid, 256);
   for (int g = tid; g < groups; g += 256) {
-    const int p = min(max(offsets[g], 0), rows);
-    const int e = min(max(offsets[g + 1], p), rows);
-    row0s[g] = p;
-    rowsg[g] = e - p;
-    tile_start[g + 1] = (DW ? mt_dw : (e - p + T - 1) / T) * nt;
+    row0s[g] = tile_start[g];
+    rowsg[g] = tile_start[g + 1] - tile_start[g];
   }
+  __syncthreads();
+  for (int g = tid; g < groups; g += 256)
+    tile_start[g + 1] = (DW ? mt_dw : (rowsg[g] + T - 1) / T) * nt;
   __syncthreads();
   if (tid < 32) {
     // inclusive scan, a run of groups per lane

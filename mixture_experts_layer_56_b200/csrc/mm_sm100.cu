@@ -34,6 +34,7 @@
 
 #include "common.cuh"
 #include "mm_sm100.h"
+#include "group_spans.cuh"
 #include "mm_ptx.cuh"
 
 namespace moe {
@@ -222,16 +223,15 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   pdl_wait();
   pdl_trigger();
   if (RAG_M || RAG_K || RAG_N) {
-    // Offsets are held to 0 <= first <= last <= rows, so that no value of
-    // them reaches outside the operands.
+    group_spans(args.offsets, G, args.rows, tile_start, tid, kThreads);
     for (int g = tid; g < G; g += kThreads) {
-      const int a = min(max(args.offsets[g], 0), args.rows);
-      const int b = min(max(args.offsets[g + 1], a), args.rows);
-      grp_row0[g] = a;
-      grp_rows[g] = b - a;
-      tile_start[g + 1] = RAG_N ? ((b - a + tn - 1) / tn) * ((args.m + kTile - 1) / kTile)
-                                : ((b - a + kTile - 1) / kTile) * nt;
+      grp_row0[g] = tile_start[g];
+      grp_rows[g] = tile_start[g + 1] - tile_start[g];
     }
+    __syncthreads();
+    for (int g = tid; g < G; g += kThreads)
+      tile_start[g + 1] = RAG_N ? ((grp_rows[g] + tn - 1) / tn) * ((args.m + kTile - 1) / kTile)
+                                : ((grp_rows[g] + kTile - 1) / kTile) * nt;
     __syncthreads();
     if (RAG_K) {
       // tiles of equal length run side by side, the longest first

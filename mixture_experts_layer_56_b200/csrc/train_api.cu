@@ -93,13 +93,15 @@ int64_t ragged_row_blocks(const moe_grouped_shape_t& s) {
 // which come in steps of 32: 64 groups of 2816 x 2048 with 12 rows each on
 // average take 116 us (0.98 of the HBM rate) for 146, with 96 rows 128 for 151,
 // with 200 rows 170 for 186.  From some 500 rows on there is nothing between
-// them but the output's transposition (16 groups of 4096 rows: 375 for 372 us).
+// them but the output's transposition (16 groups of 4096 rows: 375 for 372 us),
+// which short reductions show sooner (8 groups of 256 rows of 2048 x 256: 9.9 us
+// for 8.1).
 int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const int32_t* offsets,
                     const void* W, void* out, void* ws, int sms, cudaStream_t st) {
   using namespace sm100;
   const int32_t n = dx ? s.k : s.n, k = dx ? s.n : s.k;  // of the product
   const uint64_t k64 = k, rows = s.rows, wn = s.n, wk = s.k;
-  const bool swap = s.rows < kFewRows * s.n_groups;
+  const bool swap = s.rows < (k < 512 ? 112 : kFewRows) * s.n_groups;
   MmArgs a{};
   a.offsets = offsets;
   a.rows = static_cast<int32_t>(s.rows);
@@ -111,15 +113,21 @@ int run_ragged_rows(const moe_grouped_shape_t& s, bool dx, const void* in, const
   CUtensorMap ma, mb, tail;
   if (swap) {
     a.m = n;
-    a.tn = s.rows <= 32 ? 32 : s.rows <= 48ll * s.n_groups ? 64 : s.rows <= 112ll * s.n_groups ? 128 : 256;
+    // enough columns for most groups' rows, and fewer where that many tiles
+    // leave pairs idle
+    const int64_t some = s.rows < s.n_groups ? s.rows : s.n_groups, bands = (n + 255) / 256;
+    a.tn = s.rows <= 32                  ? 32
+           : s.rows <= 48ll * s.n_groups  ? 64
+           : s.rows <= 112ll * s.n_groups ? 128
+                                          : 256;
+    while (a.tn > 64 && bands * (s.rows / (a.tn / 2) + some) <= sms / 2) a.tn /= 2;
     const int layout = dx ? kMmTT : kMmNT;
     if (!make_map_16bit(&ma, false, W, wk, wn, s.n_groups, wk, wn * wk, mm_box_a(layout)) ||
         !make_map_16bit(&mb, false, in, k64, rows, 1, k64, rows * k64, mm_box_b(layout, a.tn)) ||
         (a.tn == 256 && !make_map_16bit(&tail, false, in, k64, rows, 1, k64, rows * k64, 32)))
       return MOE_ERR_CUDA;
-    const int64_t blocks = s.rows / a.tn + (s.rows < s.n_groups ? s.rows : s.n_groups);
     return launch_mm(layout, kMmRaggedN, kMmStoreTBf16, ma, mb, a,
-                     pairs_for(blocks * ((n + 255) / 256), sms), st, &tail);
+                     pairs_for(bands * (s.rows / a.tn + some), sms), st, &tail);
   }
   const int layout = dx ? kMmNN : kMmNT;
   a.n = n;

@@ -26,6 +26,13 @@ from . import _lib as L
 _DTYPE = {torch.bfloat16: L.MOE_DTYPE_BF16, torch.float32: L.MOE_DTYPE_F32}
 
 
+def _on_current(t, what):
+    # the library launches on the current device
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} has to be on the current CUDA device, not on {t.device}")
+    return t
+
+
 def _scratch(nbytes, device):
     # zeroed: a workspace starts with its status word
     return torch.zeros(max(256, nbytes), dtype=torch.uint8, device=device)
@@ -62,7 +69,7 @@ class TrainableExperts:
                 or t.device != self.W13.device:
             raise ValueError(f"{what} has to be contiguous [rows, {width}] of {self.dtype} beside "
                              "the weights")
-        return t
+        return _on_current(t, what)
 
     def forward(self, x: torch.Tensor, offsets: torch.Tensor, stream=None) -> torch.Tensor:
         """y[r] = FFN_g(x[r]) for the rows r of each expert g, which ``offsets``
@@ -135,6 +142,7 @@ class LayerNorm:
                 or not x.is_contiguous() or x.device != self.gamma.device:
             raise ValueError(f"rows have to be contiguous [T, {self.gamma.shape[0]}], bfloat16 or "
                              "float32, beside gamma")
+        _on_current(x, "x")
         return L.make_norm_shape(x.shape[0], x.shape[1], _DTYPE[x.dtype], self.eps)
 
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
@@ -172,6 +180,7 @@ def orthogonalize(m: torch.Tensor, steps: int = 5, coef=None, ws: torch.Tensor |
     packing permutes rows, which the iteration commutes with."""
     if m.dim() != 3 or m.dtype not in _DTYPE or not m.is_contiguous():
         raise ValueError("m has to be contiguous [n, rows, cols], bfloat16 or float32")
+    _on_current(m, "m")
     shape = L.make_ortho_shape(*m.shape, steps, _DTYPE[m.dtype])
     if ws is None:
         ws = _scratch(L.moe_orthogonalize_workspace_size(shape), m.device)

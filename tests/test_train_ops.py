@@ -181,13 +181,14 @@ def test_grouped_dw_accumulates(dtype):
 
 @pytest.mark.parametrize("dtype", BOTH)
 def test_grouped_offsets_out_of_range_are_clamped(dtype):
-    """Offsets past the rows, negative or falling reach no memory outside."""
+    """Offsets past the rows, negative or falling reach no memory outside and
+    give no row to two groups."""
     n = k = 64
     rows = 100
     g = gen(5)
     x, w = randn(g, rows, k, dtype=dtype), randn(g, 4, n, k, dtype=dtype)
     off = torch.tensor([-50, 30, 10, 4000, 2**31 - 1], dtype=torch.int32, device="cuda")
-    # clamped: [0, 30), [30, 30), [10, 100), [100, 100)
+    # taken as [0, 30), [30, 30), [30, 100), [100, 100)
     y = torch.zeros(rows, n, dtype=dtype, device="cuda")
     dw = torch.full((4, n, k), float("nan"), device="cuda", dtype=dtype)
     shape = L.make_grouped_shape(rows, 4, n, k, DT[dtype])
@@ -195,6 +196,8 @@ def test_grouped_offsets_out_of_range_are_clamped(dtype):
     L.moe_grouped_matmul(shape, x, off, w, y, ws)
     ref, tol = group_tol(x[30:].double(), w[2].double().T, k, dtype, dtype)
     assert_close(y[30:], ref, tol, "rows of group 2")
+    ref, tol = group_tol(x[:30].double(), w[0].double().T, k, dtype, dtype)
+    assert_close(y[:30], ref, tol, "rows of group 0")
     L.moe_grouped_matmul_dw(shape, y, x, off, dw, ws)
     assert (dw[1] == 0).all() and (dw[3] == 0).all() and torch.isfinite(dw.float()).all()
     assert L.moe_read_status(ws) == 0
@@ -220,6 +223,46 @@ def test_grouped_nan_stays_in_its_group(dtype):
     assert nan_rows == [45]
     assert torch.isfinite(dw[0].float()).all() and torch.isfinite(dw[2].float()).all()
     assert not torch.isfinite(dw[1].float()).all()
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("groups", [1, 31, 32, 33, 256])
+def test_grouped_with_every_number_of_groups_and_any_offsets(groups, dtype):
+    """Spans of random offsets, as the header defines them, for group counts
+    around a warp's width and at the limit."""
+    g = gen(groups)
+    rows, n, k = 500, 16, 24
+    off = torch.randint(-100, 700, (groups + 1,), generator=g, device="cuda", dtype=torch.int32)
+    held = torch.cummax(off.clamp(0, rows), 0).values.tolist()
+    x, dy = randn(g, rows, k, dtype=dtype), randn(g, rows, n, dtype=dtype)
+    w = randn(g, groups, n, k, dtype=dtype)
+    y, dx = torch.full_like(dy, 7.0), torch.full_like(x, 7.0)
+    dw = torch.full_like(w, float("nan"))
+    shape = L.make_grouped_shape(rows, groups, n, k, DT[dtype])
+    ws = clear_status(scratch(256))
+    L.moe_grouped_matmul(shape, x, off, w, y, ws)
+    L.moe_grouped_matmul_dx(shape, dy, off, w, dx, ws)
+    L.moe_grouped_matmul_dw(shape, dy, x, off, dw, ws)
+    assert (y[:held[0]] == 7).all() and (y[held[-1]:] == 7).all()
+    assert (dx[:held[0]] == 7).all() and (dx[held[-1]:] == 7).all()
+    for e, (a, b) in enumerate(zip(held[:-1], held[1:])):
+        assert_close(y[a:b], *group_tol(x[a:b].double(), w[e].double().T, k, dtype, dtype), e)
+        assert_close(dx[a:b], *group_tol(dy[a:b].double(), w[e].double(), n, dtype, dtype), e)
+        assert_close(dw[e], *group_tol(dy[a:b].double().T, x[a:b].double(), b - a, dtype, dtype), e)
+    assert L.moe_read_status(ws) == 0
+
+
+# Average rows per group on either side of every choice of tile (32, 48, 112
+# and 512 rows; widths below 256), with sizes spread around it.
+@pytest.mark.parametrize("per,n,k,groups", [(3, 320, 72, 9), (40, 264, 136, 20), (47, 512, 64, 8),
+                                            (49, 264, 200, 8), (100, 776, 64, 6), (113, 520, 136, 5),
+                                            (200, 264, 72, 7), (511, 264, 64, 3), (513, 264, 64, 3),
+                                            (700, 1040, 80, 2)])
+def test_grouped_bf16_at_every_tile_choice(per, n, k, groups):
+    g = torch.Generator().manual_seed(per)
+    sizes = torch.randint(0, 2 * per + 1, (groups,), generator=g).tolist()
+    sizes[0] += max(0, groups * per - sum(sizes))
+    run_grouped(sizes, n, k, torch.bfloat16, dirs=("fwd", "dx"))
 
 
 # ------------------------------------------------------------------- SwiGLU
@@ -607,6 +650,35 @@ def test_two_streams_at_once():
     for (t, _, _), w in zip((a, b), want):
         for k in OUTS:
             assert torch.equal(t[k], w[k]), k
+
+
+def test_first_calls_in_a_capture():
+    """A process whose first calls are captured: nothing that a call sets up
+    is left out of, or breaks, the capture."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from tests import test_train_ops as T
+t, off, step = T.training_step(T.gen(1), [40, 0, 200], 256, 64)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+first = {k: t[k].clone() for k in T.OUTS}
+for k in T.OUTS:
+    t[k].fill_(float('nan'))
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(t[k], first[k]) for k in T.OUTS)
+print('same')
+"""
+    from tests.conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_stages_are_traced():

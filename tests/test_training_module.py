@@ -25,6 +25,8 @@ def test_checks_before_any_call():
         ex.forward(torch.zeros(4, 16), off.long())
     with pytest.raises(ValueError):
         ex.forward(torch.zeros(4, 32)[:, ::2], off)
+    with pytest.raises(ValueError):
+        ex.forward(torch.zeros(4, 16), off)      # not on a GPU
     with pytest.raises(RuntimeError):
         ex.backward(torch.zeros(4, 16))
     with pytest.raises(ValueError):
@@ -34,6 +36,10 @@ def test_checks_before_any_call():
     nm = TR.LayerNorm(torch.ones(8))
     with pytest.raises(ValueError):
         nm.forward(torch.zeros(3, 9))
+    with pytest.raises(ValueError):
+        nm.forward(torch.zeros(3, 8))
+    with pytest.raises(ValueError):
+        TR.orthogonalize(torch.zeros(1, 3, 8))
     with pytest.raises(RuntimeError):
         nm.backward(torch.zeros(3, 8))
     with pytest.raises(ValueError):

@@ -267,11 +267,11 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
   const int mt_fixed = RAG_M ? 0 : (args.m + kTile - 1) / kTile;
-  // a symmetric product's block of rows mb has the column tiles up to its
-  // diagonal block, each 1 / per_blk of a block wide
+  // a symmetric product's block of rows mb has the column tiles from its
+  // diagonal block on, each 1 / per_blk of a block wide (above the diagonal,
+  // as columns come in steps of 32 where a block of few rows costs a whole one)
   const int per_blk = kTile / tn;
-  const int per_group =
-      SYM ? per_blk * (mt_fixed * (mt_fixed - 1) / 2) + nt : mt_fixed * nt;
+  const int per_group = mt_fixed * nt - (SYM ? per_blk * (mt_fixed * (mt_fixed - 1) / 2) : 0);
   const int total_tiles = RAG_M || RAG_N ? tile_start[G] : G * per_group;
 
   // position v of this pair's sequence cluster, cluster + nclusters, ...
@@ -313,12 +313,15 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const int local = t - ti.g * per_group;
       if (RAG_K) ti.g = grp_order[ti.g];
       if (SYM) {
-        const int blk = local / per_blk;
-        int mb = static_cast<int>((sqrtf(8.0f * blk + 1.0f) - 1.0f) * 0.5f);
-        while (mb * (mb + 1) / 2 > blk) --mb;
-        while ((mb + 1) * (mb + 2) / 2 <= blk) ++mb;
+        // the tiles before block row mb
+        auto before = [&](int mb) { return mb * nt - per_blk * (mb * (mb - 1) / 2); };
+        const float h = nt + 0.5f * per_blk;
+        int mb = static_cast<int>((h - sqrtf(fmaxf(h * h - 2.0f * per_blk * local, 0.0f))) / per_blk);
+        mb = min(max(mb, 0), mt_fixed - 1);
+        while (mb > 0 && before(mb) > local) --mb;
+        while (mb + 1 < mt_fixed && before(mb + 1) <= local) ++mb;
         ti.m_blk = mb;
-        ti.n_blk = local - per_blk * (mb * (mb + 1) / 2);
+        ti.n_blk = per_blk * mb + local - before(mb);
       } else {
         ti.m_blk = local / nt;
         ti.n_blk = local - ti.m_blk * nt;

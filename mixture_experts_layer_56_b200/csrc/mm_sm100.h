@@ -26,7 +26,7 @@ enum MmSched {
                    // output's transpose
   kMmRaggedK = 1,  // the reduction runs over those rows; one output per group
   kMmBatch = 2,    // `groups` equal products
-  kMmBatchSym = 3, // the same, D symmetric: only tiles on or below the diagonal
+  kMmBatchSym = 3, // the same, D symmetric: the tiles on and above the diagonal
 };
 
 enum MmEpi {
@@ -86,7 +86,7 @@ inline int32_t mm_tile_width(int32_t n, int64_t bands, int pairs) {
 inline int32_t mm_tile_width_sym(int32_t n, int64_t mats, int pairs, int64_t* tiles) {
   const int64_t blocks = (n + 255) / 256;
   auto count = [&](int32_t w) {
-    return mats * (256 / w * (blocks * (blocks - 1) / 2) + (n + w - 1) / w);
+    return mats * (blocks * ((n + w - 1) / w) - 256 / w * (blocks * (blocks - 1) / 2));
   };
   int32_t w = 256;
   while (w > 64 && count(w / 2) <= pairs) w /= 2;

@@ -18,7 +18,7 @@
 //   (D + O)(D + O) = D D + D O + O D + O O,   B X = diag(B) hi + B_off hi.
 //
 // X is held times a power of two near sqrt(max side), which centres its
-// entries in fp16's range.  A and B are symmetric: only the tiles on or below
+// entries in fp16's range.  A and B are symmetric: only the tiles on and above
 // the diagonal are computed, and written twice.
 #include <cuda.h>
 #include <cuda_fp16.h>

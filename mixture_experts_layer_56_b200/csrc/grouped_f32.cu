@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "group_spans.cuh"
 #include "train_kernels.h"
 
@@ -27,27 +28,6 @@ namespace {
 constexpr int TK = 16;
 constexpr int kFlush = 8;  // slices per inner sum
 constexpr int kMaxG = 256;
-
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-  return v;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 
 // Four neighbours p[0..3], those at or past `left` zero.
 __device__ __forceinline__ float4 load4(const float* p, int left, bool vec) {
@@ -207,7 +187,7 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
         }
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-          const uint64_t xx = pack2(x[i], x[i]);
+          const uint64_t xx = pair(x[i], x[i]);
 #pragma unroll
           for (int j = 0; j < MI / 2; ++j) acc[i][j] = fma2(xx, y[j], acc[i][j]);
         }
@@ -232,7 +212,7 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
 #pragma unroll
       for (int j = 0; j < MI / 2; ++j) {
         const int c = n0 + (j >> 1) * 64 + tx * 4 + (j & 1) * 2;
-        const float2 v = unpack2(DW ? add2(sum[i][j], acc[i][j]) : acc[i][j]);
+        const float2 v = both(DW ? add2(sum[i][j], acc[i][j]) : acc[i][j]);
         if (c < N) row[c] = accumulate ? row[c] + v.x : v.x;
         if (c + 1 < N) row[c + 1] = accumulate ? row[c + 1] + v.y : v.y;
       }

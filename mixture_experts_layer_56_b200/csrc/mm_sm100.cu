@@ -33,8 +33,9 @@
 #include <mutex>
 
 #include "common.cuh"
-#include "mm_sm100.h"
+#include "f32x2.cuh"
 #include "group_spans.cuh"
+#include "mm_sm100.h"
 #include "mm_ptx.cuh"
 
 namespace moe {
@@ -128,14 +129,24 @@ __device__ __forceinline__ uint4 pack_half8(const float* x) {
   for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
   return v;
 }
-__device__ __forceinline__ void unpack_half8(const uint4& v, float* x) {
+// eight fp16 values and four pairs
+__device__ __forceinline__ void half_pairs(const uint4& v, F2* x) {
   const __half2* h = reinterpret_cast<const __half2*>(&v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(h[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    x[i] = pair(f.x, f.y);
   }
+}
+__device__ __forceinline__ uint4 pairs_half(const F2* x) {
+  uint4 v;
+  __half2* h = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = both(x[i]);
+    h[i] = __floats2half2_rn(f.x, f.y);
+  }
+  return v;
 }
 
 struct Tile {
@@ -608,11 +619,24 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
               make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         __syncwarp();
       };
-      auto take_acc = [&](int it4, float* y) {
-        const float* p = reinterpret_cast<const float*>(
+      auto take_acc = [&](int it4, F2* y) {
+        const ulonglong2* p = reinterpret_cast<const ulonglong2*>(
             stage + (it4 * 8 + lane / 4) * kStagePitch + (lane % 4) * 32);
-        Vec16<float>::load(p, y);
-        Vec16<float>::load(p + 4, y + 4);
+        const ulonglong2 u = p[0], v = p[1];
+        y[0] = u.x;
+        y[1] = u.y;
+        y[2] = v.x;
+        y[3] = v.y;
+      };
+      // the diagonal's values at the columns of this lane's pieces of chunk c
+      auto take_diag = [&](int c, F2* d) {
+        const ulonglong2* p =
+            reinterpret_cast<const ulonglong2*>(diag_cols + c * 32 + (lane % 4) * 8);
+        const ulonglong2 u = p[0], v = p[1];
+        d[0] = u.x;
+        d[1] = u.y;
+        d[2] = v.x;
+        d[3] = v.y;
       };
       const bool empty = RAG_K && ti.nkb == 0;
       const int acc = it & 1;
@@ -761,7 +785,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
       } else if (EPI == kMmPoly) {
         // off the diagonal b a + c ((d_i + d_j) a + o), o the product of A's
-        // off-diagonal parts; on it, where a = 0, b d + c (d^2 + o)
+        // off-diagonal parts; on it, where a = 0, (b + c d) d + c o
         float* dout = args.diag_out + static_cast<int64_t>(ti.g) * args.diag_ld;
         __half* omat = static_cast<__half*>(args.out) + ti.g * args.out_stride;
         const int row0 = row - lane;
@@ -772,25 +796,33 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           uint4 out[4];
           if (col < col_end) {
             stage_acc(taddr + c * 32);
-            float dj[8];
-            Vec16<float>::load(diag_cols + c * 32 + (lane % 4) * 8, dj);
-            Vec16<float>::load(diag_cols + c * 32 + (lane % 4) * 8 + 4, dj + 4);
+            F2 dj[4];
+            take_diag(c, dj);
+            const F2 cc = pair(args.cc, args.cc);
+            const bool on = col < row0 + 32 && row0 < col + 32;  // the diagonal passes here
 #pragma unroll
             for (int it4 = 0; it4 < 4; ++it4) {
               const int pr = row0 + it4 * 8 + lane / 4;
-              float a[8], y[8];
-              unpack_half8(src_hi[c & 1].v[it4], a);
+              F2 a[4], y[4];
+              half_pairs(src_hi[c & 1].v[it4], a);
               take_acc(it4, y);
-              const float d = drow[it4];
+              const float e = args.cb + args.cc * drow[it4];  // (b + c d_i + c d_j) a + c o
+              const F2 e2 = pair(e, e);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                y[j] = args.cb * a[j] + args.cc * ((d + dj[j]) * a[j] + y[j]);
-                if (pc + j == pr) {
-                  if (pr < args.m) dout[pr] = y[j] + d * (args.cb + args.cc * d);
-                  y[j] = 0.0f;
+              for (int j = 0; j < 4; ++j)
+                y[j] = fma2(fma2(cc, dj[j], e2), a[j], mul2(cc, y[j]));
+              if (on) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float2 f = both(y[j]);
+                  const int at = pr - pc - 2 * j;  // which of the pair is on it
+                  if (at == 0 || at == 1) {
+                    if (pr < args.m) dout[pr] = (at ? f.y : f.x) + drow[it4] * e;
+                    y[j] = pair(at ? f.x : 0.0f, at ? 0.0f : f.y);
+                  }
                 }
               }
-              out[it4] = pack_half8(y);
+              out[it4] = pairs_half(y);
               if (pr < args.m && pc < ld_end)
                 *reinterpret_cast<uint4*>(omat + static_cast<int64_t>(pr) * args.ld + pc) = out[it4];
             }
@@ -834,46 +866,53 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           const int pc = col + (lane % 4) * 8;
           if (col < col_end) {
             stage_acc(taddr + c * 32);
-            float dc[8];
-            Vec16<float>::load(diag_cols + c * 32 + (lane % 4) * 8, dc);
-            Vec16<float>::load(diag_cols + c * 32 + (lane % 4) * 8 + 4, dc + 4);
+            F2 dc[4];
+            take_diag(c, dc);
+            const F2 ca = pair(args.ca, args.ca), minus = pair(-1.0f, -1.0f);
 #pragma unroll
             for (int it4 = 0; it4 < 4; ++it4) {
               const int pr = row0 + it4 * 8 + lane / 4;
-              float h[8], l[8], y[8];
-              unpack_half8(src_hi[c & 1].v[it4], h);
-              unpack_half8(src_lo[c & 1].v[it4], l);
+              F2 h[4], l[4], y[4];
+              half_pairs(src_hi[c & 1].v[it4], h);
+              half_pairs(src_lo[c & 1].v[it4], l);
               take_acc(it4, y);
+              const float e = args.ca + drow[it4];  // (a + d) hi + a lo + the product
+              const F2 e2 = pair(e, e);
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                y[j] = args.ca * (h[j] + l[j]) + (drow[it4] + dc[j]) * h[j] + y[j];
+              for (int j = 0; j < 4; ++j)
+                y[j] = fma2(add2(e2, dc[j]), h[j], fma2(ca, l[j], y[j]));
               if (pr >= args.m || pc >= ld_end) continue;
               if (!last) {
                 const int64_t at = src_base + static_cast<int64_t>(pr) * args.ld + pc;
-                const uint4 hv = pack_half8(y);
+                const uint4 hv = pairs_half(y);
                 *reinterpret_cast<uint4*>(static_cast<__half*>(args.out) + at) = hv;
-                unpack_half8(hv, h);
+                half_pairs(hv, h);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] -= h[j];
-                *reinterpret_cast<uint4*>(static_cast<__half*>(args.out_lo) + at) = pack_half8(y);
+                for (int j = 0; j < 4; ++j) y[j] = fma2(h[j], minus, y[j]);
+                *reinterpret_cast<uint4*>(static_cast<__half*>(args.out_lo) + at) = pairs_half(y);
               } else {
                 // the last step: bf16 in the caller's dense layout
                 bf16* out = static_cast<bf16*>(args.out) + ti.g * args.out_stride +
                             static_cast<int64_t>(pr) * args.n + pc;
+                float f[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] *= inv;
+                for (int j = 0; j < 4; ++j) {
+                  const float2 v = both(y[j]);
+                  f[2 * j] = v.x * inv;
+                  f[2 * j + 1] = v.y * inv;
+                }
                 if (args.vec_ok) {
-                  Vec16<bf16>::store(out, y);
+                  Vec16<bf16>::store(out, f);
                 } else if (args.n % 2 == 0) {
 #pragma unroll
                   for (int j = 0; j < 8; j += 2)
                     if (pc + j < col_end)
                       *reinterpret_cast<__nv_bfloat162*>(out + j) =
-                          __floats2bfloat162_rn(y[j], y[j + 1]);
+                          __floats2bfloat162_rn(f[j], f[j + 1]);
                 } else {
 #pragma unroll
                   for (int j = 0; j < 8; ++j)
-                    if (pc + j < col_end) out[j] = __float2bfloat16_rn(y[j]);
+                    if (pc + j < col_end) out[j] = __float2bfloat16_rn(f[j]);
                 }
               }
             }

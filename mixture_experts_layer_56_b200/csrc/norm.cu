@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "train_kernels.h"
 
 namespace moe {
@@ -26,35 +27,8 @@ template <typename T> struct NormCfg;
 template <> struct NormCfg<bf16> { static constexpr int kVals = 16; };
 template <> struct NormCfg<float> { static constexpr int kVals = 8; };
 
-// Pairs of fp32 values in 64-bit registers: Blackwell's packed arithmetic
-// halves the instructions, of which these kernels have as many as the memory
-// leaves time for.  Each half is rounded as by the scalar instruction.
-using F2 = uint64_t;
-__device__ __forceinline__ F2 pair(float x, float y) {
-  F2 v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-  return v;
-}
-__device__ __forceinline__ float2 both(F2 v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ F2 add(F2 a, F2 b) {
-  F2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-  F2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
+// Arithmetic is done on pairs: these kernels have as many instructions as the
+// memory leaves time for.
 __device__ __forceinline__ float sum_of(F2 v) {
   const float2 f = both(v);
   return f.x + f.y;
@@ -329,14 +303,14 @@ norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __rest
     // barrier, and no difference of large sums.
     F2 s = v[0];
 #pragma unroll
-    for (int i = 1; i < H; ++i) s = add(s, v[i]);
+    for (int i = 1; i < H; ++i) s = add2(s, v[i]);
     const float mu_w = warp_sum(sum_of(s)) * inv_n;
     float mu = mu_w;
     F2 m = pair(-mu, -mu);
 #pragma unroll
-    for (int i = 0; i < H; ++i) v[i] = add(v[i], m);
+    for (int i = 0; i < H; ++i) v[i] = add2(v[i], m);
     S::clip(d, t, TPR, v);
-    F2 q = mul(v[0], v[0]);
+    F2 q = mul2(v[0], v[0]);
 #pragma unroll
     for (int i = 1; i < H; ++i) q = fma2(v[i], v[i], q);
     float m2 = warp_sum(sum_of(q));
@@ -363,7 +337,7 @@ norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __rest
     m = pair(mu_w - mu, mu_w - mu);  // v is about the warp's mean already
     const F2 r2 = pair(rs, rs);
 #pragma unroll
-    for (int i = 0; i < H; ++i) v[i] = fma2(mul(add(v[i], m), r2), g[i], b[i]);
+    for (int i = 0; i < H; ++i) v[i] = fma2(mul2(add2(v[i], m), r2), g[i], b[i]);
     S::store(y + row * d, d, t, TPR, v);
     if (t == 0) {
       if (mean != nullptr) mean[row] = mu;
@@ -475,11 +449,11 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
 #pragma unroll
     for (int i = 0; i < H; ++i) {
       // past the row dy and gamma are 0, and h is not used
-      h[i] = mul(add(h[i], m), r2);
+      h[i] = mul2(add2(h[i], m), r2);
       dg[i] = fma2(v[i], h[i], dg[i]);
-      db[i] = add(db[i], v[i]);
-      v[i] = mul(v[i], g[i]);
-      a1 = add(a1, v[i]);
+      db[i] = add2(db[i], v[i]);
+      v[i] = mul2(v[i], g[i]);
+      a1 = add2(a1, v[i]);
       a2 = fma2(v[i], h[i], a2);
     }
     float s1 = sum_of(a1), s2 = sum_of(a2);
@@ -510,7 +484,7 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
       // s (v - s1 - h s2)
       const F2 c1 = pair(-s1 * inv_d, -s1 * inv_d), c2 = pair(-s2 * inv_d, -s2 * inv_d);
 #pragma unroll
-      for (int i = 0; i < H; ++i) v[i] = mul(r2, fma2(h[i], c2, add(v[i], c1)));
+      for (int i = 0; i < H; ++i) v[i] = mul2(r2, fma2(h[i], c2, add2(v[i], c1)));
       S::store(dx + row * d, d, t, TPR, v);
     }
     mu = mu_next;

@@ -19,15 +19,24 @@
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "group_spans.cuh"
+#include "sm100_ptx.cuh"
 #include "train_kernels.h"
 
 namespace moe {
 
 namespace {
 
+using namespace sm100;
+
 constexpr int TK = 16;
 constexpr int kFlush = 8;  // slices per inner sum
 constexpr int kMaxG = 256;
+
+__device__ __forceinline__ F2 ld_cluster_f2(uint32_t addr) {
+  F2 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 // Four neighbours p[0..3], those at or past `left` zero.
 __device__ __forceinline__ float4 load4(const float* p, int left, bool vec) {
@@ -80,8 +89,8 @@ struct Slice {
   }
 };
 
-template <int DIR, int MI>
-__global__ void __launch_bounds__(256, (MI == 8 && DIR != kGroupedDw) ? 2 : 1)
+template <int DIR, int MI, bool SPLIT>
+__global__ void __launch_bounds__(256, MI == 8 && DIR == kGroupedDw ? 1 : 2)
 grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
                    const int32_t* __restrict__ offsets, int groups, int rows, int n, int k,
                    float* __restrict__ out, bool accumulate) {
@@ -91,13 +100,17 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
   //   dW       M columns of dY,     N columns of X,          r over the rows
   constexpr int T = 16 * MI;
   constexpr bool FWD = DIR == kGroupedFwd, DX = DIR == kGroupedDx, DW = DIR == kGroupedDw;
-  __shared__ __align__(16) float As[2][TK][T + 4];
-  __shared__ __align__(16) float Bs[2][TK][T + 4];
+  static_assert(!SPLIT || MI * MI * 256 <= 4 * TK * (T + 4), "the sums take the slices' place");
+  __shared__ __align__(16) float slices[4][TK][T + 4];  // A's two buffers, B's two
+  float (*const As)[TK][T + 4] = slices, (*const Bs)[TK][T + 4] = slices + 2;
   __shared__ int32_t tile_start[kMaxG + 1];
   __shared__ int32_t row0s[kMaxG], rowsg[kMaxG];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
+  // The CTAs of a cluster take a tile's slices in turn.
+  const int part = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int parts = SPLIT ? static_cast<int>(gridDim.x / num_clusters_x()) : 1;
   const int N = FWD ? n : k;
   const int nt = (N + T - 1) / T;
   const int mt_dw = (n + T - 1) / T;
@@ -133,7 +146,7 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
   const int tx = tid & 15, ty = tid >> 4;
   const int64_t lda = FWD ? k : n, ldb = k;
   const bool vec_a = lda % 4 == 0, vec_b = ldb % 4 == 0;
-  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+  for (int tile = blockIdx.x / parts; tile < total; tile += gridDim.x / parts) {
     int lo = 0, hi = groups - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -156,21 +169,24 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < MI / 2; ++j) acc[i][j] = sum[i][j] = 0;
-    if (R > 0) {
-      sa.load(pa, lda, M - m0, R, vec_a, tid);
-      sb.load(pb, ldb, N - n0, R, vec_b, tid);
+    const int first = part * TK, stride = parts * TK;
+    if (first < R) {
+      pa += step_a * part;
+      pb += step_b * part;
+      sa.load(pa, lda, M - m0, R - first, vec_a, tid);
+      sb.load(pb, ldb, N - n0, R - first, vec_b, tid);
     }
     int buf = 0, cnt = 0;
-    for (int rb = 0; rb < R; rb += TK, buf ^= 1) {
+    for (int rb = first; rb < R; rb += stride, buf ^= 1) {
       sa.put(As[buf], tid);
       sb.put(Bs[buf], tid);
       // the slice before last is behind this barrier, and its buffer free
       __syncthreads();
-      if (rb + TK < R) {
-        pa += step_a;
-        pb += step_b;
-        sa.load(pa, lda, M - m0, R - rb - TK, vec_a, tid);
-        sb.load(pb, ldb, N - n0, R - rb - TK, vec_b, tid);
+      if (rb + stride < R) {
+        pa += step_a * parts;
+        pb += step_b * parts;
+        sa.load(pa, lda, M - m0, R - rb - stride, vec_a, tid);
+        sb.load(pb, ldb, N - n0, R - rb - stride, vec_b, tid);
       }
 #pragma unroll
       for (int r = 0; r < TK; ++r) {
@@ -204,32 +220,52 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
       }
     }
     __syncthreads();  // the next tile writes buffer 0 again
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
+    auto store = [&](int i, int j, F2 value) {
       const int m = m0 + (i >> 2) * 64 + ty * 4 + (i & 3);
-      if (m >= M) continue;
+      if (m >= M) return;
       float* row = DW ? out + (static_cast<int64_t>(g) * n + m) * k : out + (r0 + m) * N;
+      const int c = n0 + (j >> 1) * 64 + tx * 4 + (j & 1) * 2;
+      const float2 v = both(value);
+      if (c < N) row[c] = accumulate ? row[c] + v.x : v.x;
+      if (c + 1 < N) row[c + 1] = accumulate ? row[c + 1] + v.y : v.y;
+    };
+    if (!SPLIT) {
 #pragma unroll
-      for (int j = 0; j < MI / 2; ++j) {
-        const int c = n0 + (j >> 1) * 64 + tx * 4 + (j & 1) * 2;
-        const float2 v = both(DW ? add2(sum[i][j], acc[i][j]) : acc[i][j]);
-        if (c < N) row[c] = accumulate ? row[c] + v.x : v.x;
-        if (c + 1 < N) row[c + 1] = accumulate ? row[c + 1] + v.y : v.y;
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < MI / 2; ++j)
+          store(i, j, DW ? add2(sum[i][j], acc[i][j]) : acc[i][j]);
+    } else {
+      // the CTAs' sums are added up in order, each CTA its share of the tile
+      F2* mine = reinterpret_cast<F2*>(&slices[0][0][0]);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < MI / 2; ++j)
+          mine[(i * (MI / 2) + j) * 256 + tid] = DW ? add2(sum[i][j], acc[i][j]) : acc[i][j];
+      cluster_sync_all();
+      const int share = MI * (MI / 2) / parts;
+      for (int e = part * share; e < (part + 1) * share; ++e) {
+        const uint32_t at = smem_addr(mine + e * 256 + tid);
+        F2 v = 0;
+        for (int p = 0; p < parts; ++p) v = add2(v, ld_cluster_f2(map_to_cta(at, p)));
+        store(e / (MI / 2), e % (MI / 2), v);
       }
+      cluster_sync_all();
     }
   }
 }
 
-template <int MI>
+template <int MI, bool SPLIT>
 int launch_tiles(int dir, const float* a, const float* b, const int32_t* offsets, int groups,
                  int64_t rows, int n, int k, float* out, bool accumulate, int64_t tiles, int most,
-                 cudaStream_t st) {
-  const int grid = static_cast<int>(tiles < most ? tiles : most);
+                 int parts, cudaStream_t st) {
+  const int grid = static_cast<int>(tiles < most ? tiles : most) * parts;
   if (grid <= 0) return MOE_OK;
-  auto kern = dir == kGroupedFwd ? grouped_f32_kernel<kGroupedFwd, MI>
-              : dir == kGroupedDx ? grouped_f32_kernel<kGroupedDx, MI>
-                                  : grouped_f32_kernel<kGroupedDw, MI>;
-  return launch_k(kern, dim3(grid), dim3(256), 0, st, 1, a, b, offsets, groups,
+  auto kern = dir == kGroupedFwd ? grouped_f32_kernel<kGroupedFwd, MI, SPLIT>
+              : dir == kGroupedDx ? grouped_f32_kernel<kGroupedDx, MI, SPLIT>
+                                  : grouped_f32_kernel<kGroupedDw, MI, SPLIT>;
+  return launch_k(kern, dim3(grid), dim3(256), 0, st, parts, a, b, offsets, groups,
                   static_cast<int>(rows), n, k, out, accumulate);
 }
 
@@ -251,10 +287,18 @@ int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* o
   auto rounds = [&](int T) { return (tiles(T) + sms - 1) / sms; };
   const bool fill = dir == kGroupedDw || rows >= 96 * some;  // groups fill the large ones
   if (fill && 4.0 * rounds(128) <= 1.45 * rounds(64))
-    return launch_tiles<8>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(128),
-                           dir == kGroupedDw ? sms : 2 * sms, st);
-  return launch_tiles<4>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(64),
-                         3 * sms, st);
+    return launch_tiles<8, false>(dir, a, b, offsets, groups, rows, n, k, out, accumulate,
+                                  tiles(128), dir == kGroupedDw ? sms : 2 * sms, 1, st);
+  // Few tiles: clusters of up to 8 CTAs share a tile's reduction, four slices
+  // each at least (6 x 357 rows of 248 x 656: 46 us without).
+  const int64_t length = dir == kGroupedFwd ? k : dir == kGroupedDx ? n : rows / groups;
+  int parts = 1;
+  while (parts < 8 && tiles(64) * parts * 2 <= 4ll * sms && length >= 4ll * TK * parts * 2) parts *= 2;
+  if (parts > 1)
+    return launch_tiles<4, true>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(64),
+                                 4 * sms / parts, parts, st);
+  return launch_tiles<4, false>(dir, a, b, offsets, groups, rows, n, k, out, accumulate, tiles(64),
+                                3 * sms, 1, st);
 }
 
 }  // namespace moe

@@ -257,12 +257,21 @@ def test_grouped_with_every_number_of_groups_and_any_offsets(groups, dtype):
 @pytest.mark.parametrize("per,n,k,groups", [(3, 320, 72, 9), (40, 264, 136, 20), (47, 512, 64, 8),
                                             (49, 264, 200, 8), (100, 776, 64, 6), (113, 520, 136, 5),
                                             (200, 264, 72, 7), (511, 264, 64, 3), (513, 264, 64, 3),
-                                            (700, 1040, 80, 2)])
+                                            (700, 1040, 80, 2), (130, 600, 512, 6), (200, 520, 776, 7),
+                                            (300, 1288, 520, 4)])
 def test_grouped_bf16_at_every_tile_choice(per, n, k, groups):
     g = torch.Generator().manual_seed(per)
     sizes = torch.randint(0, 2 * per + 1, (groups,), generator=g).tolist()
     sizes[0] += max(0, groups * per - sum(sizes))
     run_grouped(sizes, n, k, torch.bfloat16, dirs=("fwd", "dx"))
+
+
+@pytest.mark.parametrize("sizes,n,k", [([300, 0, 129], 70, 300), ([700], 33, 520),
+                                       ([40] * 5, 520, 264), ([3], 17, 2000), ([2500, 1], 130, 70),
+                                       ([900, 0, 800], 520, 136)])
+def test_grouped_f32_few_tiles_and_long_sums(sizes, n, k):
+    """Clusters share a tile's reduction, or 128 x 128 tiles."""
+    run_grouped(sizes, n, k, torch.float32, lead=1, tail=2)
 
 
 # ------------------------------------------------------------------- SwiGLU

@@ -16,8 +16,13 @@ A step of the layer's training is made of
     du = norm.backward(dx)                   # dx = sums of dx_rows by token
     m = beta * m + experts.dW13              # the optimiser's momentum
     update = orthogonalize(m)
+
+Each call runs on ``stream`` (a torch stream or a raw handle; None: the current
+one), and so does every allocation that it makes, its results among them.
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -31,6 +36,19 @@ def _on_current(t, what):
     if not t.is_cuda or t.device.index != torch.cuda.current_device():
         raise ValueError(f"{what} has to be on the current CUDA device, not on {t.device}")
     return t
+
+
+def _on(stream):
+    """A context in which torch allocates for ``stream``."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _same_stream(saved, stream):
+    # the saved tensors return to their stream's pool with the backward pass
+    if L._stream(stream) != saved:
+        raise ValueError("backward() on another stream than its forward()")
 
 
 def _scratch(nbytes, device):
@@ -74,19 +92,22 @@ class TrainableExperts:
     def forward(self, x: torch.Tensor, offsets: torch.Tensor, stream=None) -> torch.Tensor:
         """y[r] = FFN_g(x[r]) for the rows r of each expert g, which ``offsets``
         (int32 [n + 1], of ``moe_dispatch``) gives.  Keeps what ``backward``
-        needs: x and offsets themselves, which must not change before it."""
+        needs: x and offsets themselves, which must not change before it, on
+        the same stream."""
         self._rows(x, self.d, "x")
         if offsets.dtype != torch.int32 or offsets.shape != (self.n + 1,) \
                 or offsets.device != x.device or not offsets.is_contiguous():
             raise ValueError(f"offsets has to be contiguous int32 [{self.n + 1}] beside the weights")
         rows = x.shape[0]
-        gu, a, y = x.new_empty(rows, 2 * self.inter), x.new_empty(rows, self.inter), torch.empty_like(x)
+        with _on(stream):
+            gu, a = x.new_empty(rows, 2 * self.inter), x.new_empty(rows, self.inter)
+            y = torch.empty_like(x)
         L.moe_grouped_matmul(self._shape(rows, 2 * self.inter, self.d), x, offsets, self.W13, gu,
                              self.ws, stream=stream)
         L.moe_swiglu(L.make_swiglu_shape(rows, self.inter, _DTYPE[self.dtype]), gu, a, stream=stream)
         L.moe_grouped_matmul(self._shape(rows, self.d, self.inter), a, offsets, self.W2, y, self.ws,
                              stream=stream)
-        self._saved = (x, offsets, gu, a)
+        self._saved = (x, offsets, gu, a, L._stream(stream))
         return y
 
     def backward(self, dy: torch.Tensor, stream=None) -> torch.Tensor:
@@ -94,9 +115,10 @@ class TrainableExperts:
         dW2.  Once per forward."""
         if self._saved is None:
             raise RuntimeError("backward() without a forward() before it")
-        x, offsets, gu, a = self._saved
+        x, offsets, gu, a, saved_on = self._saved
         if self._rows(dy, self.d, "dy").shape != x.shape:
             raise ValueError("dy has to have as many rows as x")
+        _same_stream(saved_on, stream)
         self._saved = None
         rows, flags = x.shape[0], L.MOE_GROUPED_DW_F32
         if self._have_grad:
@@ -104,7 +126,8 @@ class TrainableExperts:
         self._have_grad = True
         up = self._shape(rows, 2 * self.inter, self.d, flags)
         down = self._shape(rows, self.d, self.inter, flags)
-        da, dx = torch.empty_like(a), torch.empty_like(x)
+        with _on(stream):
+            da, dx = torch.empty_like(a), torch.empty_like(x)
         L.moe_grouped_matmul_dx(down, dy, offsets, self.W2, da, self.ws, stream=stream)
         L.moe_grouped_matmul_dw(down, dy, a, offsets, self.dW2, self.ws, stream=stream)
         # the pre-activations' gradient takes their place
@@ -135,7 +158,6 @@ class LayerNorm:
         self.dgamma = torch.empty_like(gamma)
         self.dbeta = None if beta is None else torch.empty_like(beta)
         self._saved = None
-        self._ws = None
 
     def _shape(self, x):
         if x.dim() != 2 or x.shape[1] != self.gamma.shape[0] or x.dtype not in _DTYPE \
@@ -146,30 +168,33 @@ class LayerNorm:
         return L.make_norm_shape(x.shape[0], x.shape[1], _DTYPE[x.dtype], self.eps)
 
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
-        """Keeps x itself, which must not change before ``backward``."""
+        """Keeps x itself, which must not change before ``backward``, on the
+        same stream."""
         shape = self._shape(x)
-        y = torch.empty_like(x)
-        mean = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
+        with _on(stream):
+            y = torch.empty_like(x)
+            mean = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+            rstd = torch.empty_like(mean)
         L.moe_layer_norm(shape, x, self.gamma, self.beta, y, mean, rstd, stream=stream)
-        self._saved = (x, mean, rstd)
+        self._saved = (x, mean, rstd, L._stream(stream))
         return y
 
     def backward(self, dy: torch.Tensor, stream=None) -> torch.Tensor:
         """The gradient of ``forward``'s x; writes dgamma and dbeta."""
         if self._saved is None:
             raise RuntimeError("backward() without a forward() before it")
-        x, mean, rstd = self._saved
+        x, mean, rstd, saved_on = self._saved
         shape = self._shape(dy)
         if dy.shape != x.shape or dy.dtype != x.dtype:
             raise ValueError("dy has to be like x")
+        _same_stream(saved_on, stream)
         self._saved = None
-        need = L.moe_layer_norm_workspace_size(shape)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = _scratch(need, x.device)
-        dx = torch.empty_like(x)
+        with _on(stream):
+            dx = torch.empty_like(x)
+            # a workspace per call: captured ones may replay side by side
+            ws = x.new_empty(max(256, L.moe_layer_norm_workspace_size(shape)), dtype=torch.uint8)
         L.moe_layer_norm_backward(shape, dy, x, self.gamma, mean, rstd, dx, self.dgamma, self.dbeta,
-                                  self._ws, stream=stream)
+                                  ws, stream=stream)
         return dx
 
 
@@ -182,8 +207,9 @@ def orthogonalize(m: torch.Tensor, steps: int = 5, coef=None, ws: torch.Tensor |
         raise ValueError("m has to be contiguous [n, rows, cols], bfloat16 or float32")
     _on_current(m, "m")
     shape = L.make_ortho_shape(*m.shape, steps, _DTYPE[m.dtype])
-    if ws is None:
-        ws = _scratch(L.moe_orthogonalize_workspace_size(shape), m.device)
-    o = torch.empty(m.shape, dtype=torch.bfloat16, device=m.device)
+    with _on(stream):
+        if ws is None:
+            ws = _scratch(L.moe_orthogonalize_workspace_size(shape), m.device)
+        o = torch.empty(m.shape, dtype=torch.bfloat16, device=m.device)
     L.moe_orthogonalize(shape, m, o, ws, coef=coef, stream=stream)
     return o

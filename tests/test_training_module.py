@@ -178,3 +178,82 @@ def test_a_layer_step_with_the_norm_and_its_gradient(TR):
     assert float((h.double() - hd).norm() / hd.norm()) <= 6 * 2.0 ** -8
     want = ud.grad - dh.double()
     assert float((du.double() - want).norm() / want.norm()) <= 9 * 2.0 ** -8
+
+
+def _steps(TR):
+    """A forward and backward of the norm and the experts, and an update, over
+    the same inputs: a function of the stream."""
+    g = torch.Generator(device="cuda").manual_seed(23)
+
+    def rnd(*s, scale=1.0):
+        return (torch.randn(*s, generator=g, device="cuda") * scale).bfloat16()
+
+    w13, w2 = rnd(4, 512, 192, scale=0.1), rnd(4, 192, 256, scale=0.1)
+    gamma, beta = rnd(192).float(), rnd(192).float()
+    u, dy, m = rnd(600, 192), rnd(600, 192), rnd(2, 200, 300)
+    off = torch.tensor([0, 100, 100, 450, 600], dtype=torch.int32, device="cuda")
+
+    def run(stream=None):
+        ex, nm = TR.TrainableExperts(w13, w2), TR.LayerNorm(gamma, beta)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(200_000_000)  # some 100 ms: what follows runs late
+        x = nm.forward(u, stream=stream)
+        y = ex.forward(x, off, stream=stream)
+        dx = ex.backward(dy, stream=stream)
+        du = nm.backward(dx, stream=stream)
+        o = TR.orthogonalize(m, stream=stream)
+        return [y, dx, du, o, ex.dW13, ex.dW2, nm.dgamma, nm.dbeta], (ex, nm)
+
+    return run
+
+
+@pytest.mark.gpu
+def test_a_stream_of_its_own_keeps_its_temporaries(TR):
+    """What the calls allocate for themselves belongs to the stream they run
+    on: the current stream neither gets that memory while they run, nor do they
+    write into what it got."""
+    run = _steps(TR)
+    want, _ = run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+
+    def fill():
+        # every size that the calls allocate
+        return ([torch.full((600, c), 7.0, dtype=torch.bfloat16, device="cuda")
+                 for c in (192, 256, 512) for _ in range(8)]
+                + [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+                   for n in (2400, 1 << 14, 1 << 17, 1 << 20, 1 << 21) for _ in range(4)])
+
+    fill()  # its kernels are loaded, its memory is in the pool
+    torch.cuda.synchronize()
+    got, keep = run(side)
+    late = not side.query()
+    junk = fill()
+    assert late, "the side stream was done before the current one could get in its way"
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for t in junk:
+        assert (t == (7.0 if t.is_floating_point() else 255)).all()
+    assert keep[0].status() == 0
+
+
+@pytest.mark.gpu
+def test_backward_on_another_stream_than_its_forward(TR):
+    u = torch.randn(8, 64, device="cuda")
+    nm = TR.LayerNorm(torch.ones(64, device="cuda"))
+    nm.forward(u)
+    with pytest.raises(ValueError, match="stream"):
+        nm.backward(u, stream=torch.cuda.Stream())
+    nm.backward(u)  # and the forward is still there
+    ex = TR.TrainableExperts(torch.ones(1, 128, 64, device="cuda"),
+                             torch.ones(1, 64, 64, device="cuda"))
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    ex.forward(u, off)
+    with pytest.raises(ValueError, match="stream"):
+        ex.backward(u, stream=torch.cuda.Stream().cuda_stream)
+    ex.backward(u)
+    torch.cuda.synchronize()

@@ -186,14 +186,29 @@ constexpr int fwd_blocks(int tpr) {
 constexpr int bwd_blocks(int tpr) { return at_least_1(512 / block_threads(tpr)); }
 
 // Rows on their way from memory: kRing rows per group, of each of the ARRAYS
-// that a pass reads, in shared memory, fetched with cp.async.  A thread copies exactly the values that it
-// will use, so that its own wait_group is all the waiting there is.
+// that a pass reads, in shared memory, fetched with cp.async.  A thread whose
+// values are whole 16-byte pieces or fp32 copies exactly those, so that its own
+// wait_group is all the waiting there is.  Rows of bf16 that start anywhere in a
+// piece: the group copies the pieces that the row touches, up to the tensor's
+// end, and a thread finds its values behind a barrier (kShared; 8192 x 4099
+// forward 54 us, 71 with each thread loading its own as it needs them), except
+// where a row is a warp's, whose many rows in flight do the same for less
+// (kDirect; 65536 x 131 backward 35 us for 45).  With two or eight values of
+// such a row per access and their realignment in registers it takes longer, as
+// these kernels are bound by their instructions.
 constexpr int kRing = 3;
 
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                    static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
                "l"(src)
+               : "memory");
+}
+// the first `bytes` of the 16, zeros behind them
+__device__ __forceinline__ void copy_async_first(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copy_async4(void* dst, const void* src) {
@@ -211,47 +226,76 @@ template <typename T, bool VEC, int TPR, int ARRAYS>
 struct RowRing {
   using S = RowSlice<T, VEC>;
   static constexpr int B = block_of<TPR>();
-  // odd widths of 2-byte values have no 4-byte alignment: loaded directly
-  static constexpr bool kAsync = VEC || sizeof(T) == 4;
-  static constexpr int kBytes = kAsync ? kRing * ARRAYS * S::V * B * static_cast<int>(sizeof(T)) : 0;
+  static constexpr bool kAnywhere = !VEC && sizeof(T) == 2;
+  static constexpr bool kShared = kAnywhere && TPR > 32, kDirect = kAnywhere && TPR == 32;
+  static constexpr int kRow = S::V * TPR * static_cast<int>(sizeof(T)) + (kShared ? 32 : 0);
+  static constexpr int kBytes = kDirect ? 0 : kRing * ARRAYS * (B / TPR) * kRow;
 
-  __device__ __forceinline__ static T* slot(uint8_t* base, int stage, int which, int i) {
-    // 16-byte pieces (VEC) or single values of all threads side by side
+  // a thread's 16-byte pieces (VEC) or single values, those of all threads side by side
+  __device__ __forceinline__ static T* own(uint8_t* base, int stage, int which, int i) {
     constexpr int N = VEC ? S::N : 1;
     return reinterpret_cast<T*>(base) +
-           (static_cast<size_t>((stage * ARRAYS + which) * (S::V / N) + i) * B + threadIdx.x) * N;
+           (((stage * ARRAYS + which) * (S::V / N) + i) * B + threadIdx.x) * N;
   }
+  // kShared: this group's row
+  __device__ __forceinline__ static uint8_t* row(uint8_t* base, int stage, int which) {
+    return base + ((stage * ARRAYS + which) * (B / TPR) + threadIdx.x / TPR) * kRow;
+  }
+  // the row at p of a tensor that ends at `end`
   __device__ __forceinline__ static void fetch(uint8_t* base, int stage, int which, const T* p,
-                                               int d, int t) {
+                                               const T* end, int d, int t) {
+    if (kDirect) return;
     if (VEC) {
 #pragma unroll
       for (int i = 0; i < S::P; ++i) {
         const int c = (t + i * TPR) * S::N;
-        if (c < d) copy_async16(slot(base, stage, which, i), p + c);
+        if (c < d) copy_async16(own(base, stage, which, i), p + c);
+      }
+    } else if (kShared) {
+      const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(p) - skip;
+      const int64_t left = reinterpret_cast<const uint8_t*>(end) - from;
+      const int bytes = skip + d * static_cast<int>(sizeof(T));
+      uint8_t* to = row(base, stage, which);
+#pragma unroll
+      for (int i = 0; i <= S::P; ++i) {
+        const int at = (t + i * TPR) * 16;
+        if (at < bytes)
+          copy_async_first(to + at, from + at, left - at < 16 ? static_cast<int>(left - at) : 16);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < S::V; ++i) {
         const int c = t + i * TPR;
-        if (c < d) copy_async4(slot(base, stage, which, i), p + c);
+        if (c < d) copy_async4(own(base, stage, which, i), p + c);
       }
     }
   }
-  __device__ __forceinline__ static void take(uint8_t* base, int stage, int which, int d, int t,
-                                              F2* v) {
+  // a row's copies have landed, for every thread that takes from them
+  __device__ __forceinline__ static void landed() {
+    if (!kDirect) copy_wait<kRing - 1>();
+    if (kShared) __syncthreads();
+  }
+  __device__ __forceinline__ static void take(uint8_t* base, int stage, int which, const T* p, int d,
+                                              int t, F2* v) {
     if (VEC) {
 #pragma unroll
       for (int i = 0; i < S::P; ++i) {
         uint4 w = make_uint4(0, 0, 0, 0);
         if ((t + i * TPR) * S::N < d)
-          w = *reinterpret_cast<const uint4*>(slot(base, stage, which, i));
+          w = *reinterpret_cast<const uint4*>(own(base, stage, which, i));
         piece_pairs(w, v + i * S::PP, T());
       }
+    } else if (kDirect || kShared) {
+      const T* s = kDirect ? p
+                           : reinterpret_cast<const T*>(row(base, stage, which) +
+                                                        (reinterpret_cast<uintptr_t>(p) & 15));
+      S::load(s, d, t, TPR, v);
     } else {
 #pragma unroll
       for (int i = 0; i < S::V; i += 2)
-        v[i / 2] = pair(t + i * TPR < d ? to_f32(*slot(base, stage, which, i)) : 0.0f,
-                        t + (i + 1) * TPR < d ? to_f32(*slot(base, stage, which, i + 1)) : 0.0f);
+        v[i / 2] = pair(t + i * TPR < d ? to_f32(*own(base, stage, which, i)) : 0.0f,
+                        t + (i + 1) * TPR < d ? to_f32(*own(base, stage, which, i + 1)) : 0.0f);
     }
   }
 };
@@ -276,8 +320,8 @@ norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __rest
   const int64_t step = static_cast<int64_t>(gridDim.x) * RG;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * RG + grp;
   auto fetch = [&](int64_t row, int stage) {
-    if (R::kAsync && row < rows) R::fetch(ring, stage, 0, x + row * d, d, t);
-    if (R::kAsync) copy_commit();
+    if (row < rows) R::fetch(ring, stage, 0, x + row * d, x + rows * d, d, t);
+    copy_commit();
   };
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) fetch(first + s * step, s);
@@ -306,14 +350,8 @@ norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __rest
     F2 v[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) v[i] = 0;
-    if (live) {
-      if (R::kAsync) {
-        copy_wait<kRing - 1>();
-        R::take(ring, stage, 0, d, t, v);
-      } else {
-        S::load(x + row * d, d, t, TPR, v);
-      }
-    }
+    R::landed();
+    if (live) R::take(ring, stage, 0, x + row * d, d, t, v);
     stage = (stage + 1) % kRing;
     // each warp takes its values' mean and squares about it, and the warps of
     // a row then join theirs: M2 = sum M2_w + n_w (mean_w - mean)^2.  One
@@ -355,8 +393,21 @@ norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __rest
   }
 }
 
-// Rows that the registers do not hold: three reads of x.
-template <typename T>
+// `n` values from p (16-byte pieces where n is more than 1).
+template <int n, typename T>
+__device__ __forceinline__ void load_n(const T* p, float* v) {
+  if (n == 1) {
+    v[0] = to_f32(*p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; i += Vec16<T>::N) Vec16<T>::load(p + i, v + i);
+  }
+}
+
+// Rows that the registers do not hold: three reads of x, the last two from L1
+// and L2 (8192 x 16384 bf16 forward 129 us, 4.2 TB/s; backward 265 us).  N values
+// per access: a 16-byte piece, or one where rows are not whole pieces.
+template <typename T, int N>
 __global__ void __launch_bounds__(512)
 norm_fwd_wide_kernel(const T* x, const float* __restrict__ gamma,
                      const float* __restrict__ beta, int d, float eps, T* y,
@@ -366,18 +417,36 @@ norm_fwd_wide_kernel(const T* x, const float* __restrict__ gamma,
   pdl_trigger();
   const int64_t row = blockIdx.x;
   const T* p = x + row * d;
-  float s = 0.0f;
-  for (int c = threadIdx.x; c < d; c += 512) s += to_f32(p[c]);
+  float s = 0.0f, v[N];
+#pragma unroll 4
+  for (int c = threadIdx.x * N; c < d; c += 512 * N) {
+    load_n<N>(p + c, v);
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) t += v[i];
+    s += t;
+  }
   const float mu = block_sum512(s, red[0]) / d;
   float q = 0.0f;
-  for (int c = threadIdx.x; c < d; c += 512) {
-    const float h = to_f32(p[c]) - mu;
-    q += h * h;
+#pragma unroll 4
+  for (int c = threadIdx.x * N; c < d; c += 512 * N) {
+    load_n<N>(p + c, v);
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) t += (v[i] - mu) * (v[i] - mu);
+    q += t;
   }
   const float rs = 1.0f / sqrtf(block_sum512(q, red[1]) / d + eps);
-  for (int c = threadIdx.x; c < d; c += 512) {
-    const float h = (to_f32(p[c]) - mu) * rs * gamma[c];
-    y[row * d + c] = from_f32<T>(beta != nullptr ? h + beta[c] : h);
+#pragma unroll(N > 1 ? 2 : 4)
+  for (int c = threadIdx.x * N; c < d; c += 512 * N) {
+    float g[N], b[N] = {};
+    load_n<N>(p + c, v);
+    load_n<N>(gamma + c, g);
+    if (beta != nullptr) load_n<N>(beta + c, b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = (v[i] - mu) * rs * g[i] + b[i];
+    if (N == 1) y[row * d + c] = from_f32<T>(v[0]);
+    else Vec16<T>::store(y + row * d + c, v);
   }
   if (threadIdx.x == 0) {
     if (mean != nullptr) mean[row] = mu;
@@ -411,11 +480,11 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
   const int64_t step = static_cast<int64_t>(gridDim.x) * RG;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * RG + grp;
   auto fetch = [&](int64_t row, int stage) {
-    if (R::kAsync && row < rows) {
-      R::fetch(ring, stage, 0, x + row * d, d, t);
-      R::fetch(ring, stage, 1, dy + row * d, d, t);
+    if (row < rows) {
+      R::fetch(ring, stage, 0, x + row * d, x + rows * d, d, t);
+      R::fetch(ring, stage, 1, dy + row * d, dy + rows * d, d, t);
     }
-    if (R::kAsync) copy_commit();
+    copy_commit();
   };
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) fetch(first + s * step, s);
@@ -442,15 +511,10 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
     F2 h[H], v[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) h[i] = v[i] = 0;
+    R::landed();
     if (live) {
-      if (R::kAsync) {
-        copy_wait<kRing - 1>();
-        R::take(ring, stage, 0, d, t, h);
-        R::take(ring, stage, 1, d, t, v);
-      } else {
-        S::load(x + row * d, d, t, TPR, h);
-        S::load(dy + row * d, d, t, TPR, v);
-      }
+      R::take(ring, stage, 0, x + row * d, d, t, h);
+      R::take(ring, stage, 1, dy + row * d, d, t, v);
     }
     stage = (stage + 1) % kRing;
     const F2 m = pair(-mu, -mu), r2 = pair(rs, rs);
@@ -533,7 +597,7 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
 }
 
 // Wide rows: dx in one kernel (two reads of x and dy; dx may be dy) ...
-template <typename T>
+template <typename T, int N>
 __global__ void __launch_bounds__(512)
 norm_bwd_wide_kernel(const T* dy, const T* __restrict__ x,
                      const float* __restrict__ gamma, const float* __restrict__ mean,
@@ -543,39 +607,64 @@ norm_bwd_wide_kernel(const T* dy, const T* __restrict__ x,
   pdl_trigger();
   const int64_t row = blockIdx.x;
   const float mu = mean[row], rs = rstd[row];
-  float s1 = 0.0f, s2 = 0.0f;
-  for (int c = threadIdx.x; c < d; c += 512) {
-    const float v = to_f32(dy[row * d + c]) * gamma[c];
-    s1 += v;
-    s2 += v * ((to_f32(x[row * d + c]) - mu) * rs);
+  float s1 = 0.0f, s2 = 0.0f, h[N], v[N], g[N];
+#pragma unroll(N > 1 ? 2 : 4)
+  for (int c = threadIdx.x * N; c < d; c += 512 * N) {
+    load_n<N>(x + row * d + c, h);
+    load_n<N>(dy + row * d + c, v);
+    load_n<N>(gamma + c, g);
+    float t1 = 0.0f, t2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float w = v[i] * g[i];
+      t1 += w;
+      t2 += w * ((h[i] - mu) * rs);
+    }
+    s1 += t1;
+    s2 += t2;
   }
   s1 = block_sum512(s1, red[0]) / d;
   s2 = block_sum512(s2, red[1]) / d;
-  for (int c = threadIdx.x; c < d; c += 512) {
-    const float v = to_f32(dy[row * d + c]) * gamma[c];
-    const float h = (to_f32(x[row * d + c]) - mu) * rs;
-    dx[row * d + c] = from_f32<T>(rs * (v - s1 - h * s2));
+#pragma unroll(N > 1 ? 2 : 4)
+  for (int c = threadIdx.x * N; c < d; c += 512 * N) {
+    load_n<N>(x + row * d + c, h);
+    load_n<N>(dy + row * d + c, v);
+    load_n<N>(gamma + c, g);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = rs * (v[i] * g[i] - s1 - (h[i] - mu) * rs * s2);
+    if (N == 1) dx[row * d + c] = from_f32<T>(v[0]);
+    else Vec16<T>::store(dx + row * d + c, v);
   }
 }
 
-// ... and the column sums in another, a thread per column and slice of rows.
-template <typename T>
+// ... and the column sums in another, a thread per N columns and slice of rows.
+template <typename T, int N>
 __global__ void __launch_bounds__(256)
 norm_bwd_cols_kernel(const T* __restrict__ dy, const T* __restrict__ x,
                      const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows,
                      int d, float* __restrict__ part) {
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x * 256 + threadIdx.x;
+  const int c = (blockIdx.x * 256 + threadIdx.x) * N;
   if (c >= d) return;
-  float g = 0.0f, b = 0.0f;
+  float g[N] = {}, b[N] = {};
+#pragma unroll 4
   for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-    const float v = to_f32(dy[row * d + c]);
-    g += v * ((to_f32(x[row * d + c]) - mean[row]) * rstd[row]);
-    b += v;
+    float v[N], h[N];
+    load_n<N>(dy + row * d + c, v);
+    load_n<N>(x + row * d + c, h);
+    const float mu = mean[row], rs = rstd[row];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      g[i] += v[i] * ((h[i] - mu) * rs);
+      b[i] += v[i];
+    }
   }
-  part[static_cast<int64_t>(blockIdx.y) * d + c] = g;
-  part[(static_cast<int64_t>(gridDim.y) + blockIdx.y) * d + c] = b;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    part[static_cast<int64_t>(blockIdx.y) * d + c + i] = g[i];
+    part[(static_cast<int64_t>(gridDim.y) + blockIdx.y) * d + c + i] = b[i];
+  }
 }
 
 // dgamma, dbeta = column sums of the blocks' partial rows, 32 columns by 32
@@ -647,7 +736,7 @@ int fwd_group(const T* x, const float* gamma, const float* beta, int64_t rows, i
     case 384: return fwd_impl<T, VEC, 384>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
     case 512: return fwd_impl<T, VEC, 512>(x, gamma, beta, rows, d, eps, y, mean, rstd, sms, st);
   }
-  return launch_k(norm_fwd_wide_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, 1,
+  return launch_k(norm_fwd_wide_kernel<T, VEC ? Vec16<T>::N : 1>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, 1,
                   x, gamma, beta, d, eps, y, mean, rstd);
 }
 
@@ -684,10 +773,11 @@ int bwd_group(const T* dy, const T* x, const float* gamma, const float* mean, co
     case 512: return bwd_impl<T, VEC, 512>(dy, x, gamma, mean, rstd, rows, d, dx, part, part_rows, st);
   }
   // the column sums first: dx may be dy
-  if (int rc = launch_k(norm_bwd_cols_kernel<T>, dim3((d + 255) / 256, part_rows), dim3(256), 0, st,
-                        1, dy, x, mean, rstd, rows, d, part))
+  constexpr int N = VEC ? Vec16<T>::N : 1;
+  if (int rc = launch_k(norm_bwd_cols_kernel<T, N>, dim3((d + 256 * N - 1) / (256 * N), part_rows),
+                        dim3(256), 0, st, 1, dy, x, mean, rstd, rows, d, part))
     return rc;
-  return launch_k(norm_bwd_wide_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, 1,
+  return launch_k(norm_bwd_wide_kernel<T, N>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, 1,
                   dy, x, gamma, mean, rstd, d, dx);
 }
 

@@ -173,17 +173,28 @@ __device__ __forceinline__ float block_sum512(float v, float* red) {
   return v;
 }
 
-// Threads of a block: whole groups, about 256; and blocks per SM in the forward
-// and the backward kernel: what the registers allow, or fewer where more were
-// slower (32768 x 2048 forward: 58 us with three blocks, 52 with two; x 4096:
-// 88 with three, 101 with two).
 constexpr int block_threads(int tpr) { return tpr > 256 ? tpr : 256 / tpr * tpr; }
 template <int TPR> constexpr int block_of() { return block_threads(TPR); }
+// Threads of a block: whole groups, about 256; and blocks per SM in the forward
+// and the backward kernel: what the registers allow, or fewer where more were
+// slower.  bf16 forward, 65536 x 1536: 87 us with four blocks, 78 with three;
+// 32768 x 2048: 57 with three, 53 with two; x 4096: 88 with three, 101 with two.
+// fp32, whose threads hold half the values: 32768 x 1000 forward 56 us with two
+// blocks, 45 with three, backward 69 and 63.
 constexpr int at_least_1(int v) { return v > 1 ? v : 1; }
-constexpr int fwd_blocks(int tpr) {
-  return at_least_1((tpr == 128 ? 512 : 768) / block_threads(tpr));
+template <typename T> constexpr int fwd_blocks(int tpr) {
+  const bool few = sizeof(T) == 2 && tpr >= 64 && tpr <= 128;
+  return at_least_1((!few ? 768 : tpr == 96 ? 576 : 512) / block_threads(tpr));
 }
-constexpr int bwd_blocks(int tpr) { return at_least_1(512 / block_threads(tpr)); }
+template <typename T> constexpr int bwd_blocks(int tpr) {
+  return at_least_1((sizeof(T) == 2 ? 512 : tpr == 96 ? 576 : 768) / block_threads(tpr));
+}
+// Barrier of a row's group of TPR threads, whole warps, in its block.
+template <int TPR>
+__device__ __forceinline__ void group_sync() {
+  if (block_of<TPR>() == TPR) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / TPR), "n"(TPR) : "memory");
+}
 
 // Rows on their way from memory: kRing rows per group, of each of the ARRAYS
 // that a pass reads, in shared memory, fetched with cp.async.  A thread whose
@@ -274,7 +285,7 @@ struct RowRing {
   // a row's copies have landed, for every thread that takes from them
   __device__ __forceinline__ static void landed() {
     if (!kDirect) copy_wait<kRing - 1>();
-    if (kShared) __syncthreads();
+    if (kShared) group_sync<TPR>();
   }
   __device__ __forceinline__ static void take(uint8_t* base, int stage, int which, const T* p, int d,
                                               int t, F2* v) {
@@ -301,7 +312,7 @@ struct RowRing {
 };
 
 template <typename T, bool VEC, int TPR>
-__global__ void __launch_bounds__(block_of<TPR>(), fwd_blocks(TPR))
+__global__ void __launch_bounds__(block_of<TPR>(), fwd_blocks<T>(TPR))
 norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __restrict__ beta,
                 int64_t rows, int d, float eps, T* y, float* __restrict__ mean,
                 float* __restrict__ rstd) {
@@ -372,7 +383,7 @@ norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __rest
     if (W > 1) {
       // a lane for each warp of the row
       if (lane == 0) red[buf][warp] = make_float2(mu, m2);
-      __syncthreads();
+      group_sync<TPR>();
       const float2 of = lane < W ? red[buf][w0 + lane] : make_float2(0.0f, 0.0f);
       const float x0 = __shfl_sync(0xffffffffu, of.x, 0);
       mu = x0 + lanes_sum<W>(n_lane * (of.x - x0)) * inv_d;  // of the row
@@ -462,7 +473,7 @@ constexpr int bwd_smem() {
 }
 
 template <typename T, bool VEC, int TPR>
-__global__ void __launch_bounds__(block_of<TPR>(), bwd_blocks(TPR))
+__global__ void __launch_bounds__(block_of<TPR>(), bwd_blocks<T>(TPR))
 norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ gamma,
                 const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows,
                 int d, T* dx, float* __restrict__ part) {
@@ -538,7 +549,7 @@ norm_bwd_kernel(const T* dy, const T* __restrict__ x, const float* __restrict__ 
       constexpr int W = TPR / 32;
       const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
       if (lane == 0) red[buf][warp] = make_float2(s1, s2);
-      __syncthreads();
+      group_sync<TPR>();
       const float2 of = lane < W ? red[buf][warp / W * W + lane] : make_float2(0.0f, 0.0f);
       s1 = lanes_sum<W>(of.x);
       s2 = lanes_sum<W>(of.y);
@@ -706,7 +717,7 @@ int part_rows_of(int64_t T_, int d, int sms) {
   if (tpr == 0) return static_cast<int>(T_ < 64 ? T_ : 64);
   const int rg = block_threads(tpr) / tpr;
   const int64_t blocks = (T_ + rg - 1) / rg;
-  const int64_t most = static_cast<int64_t>(sms) * bwd_blocks(tpr);
+  const int64_t most = static_cast<int64_t>(sms) * bwd_blocks<T>(tpr);
   return static_cast<int>(blocks < most ? blocks : most);
 }
 
@@ -718,7 +729,7 @@ int fwd_impl(const T* x, const float* gamma, const float* beta, int64_t rows, in
   static std::atomic<uint64_t> optin{0};
   auto kern = norm_fwd_kernel<T, VEC, TPR>;
   if (int rc = ensure_smem_optin(reinterpret_cast<const void*>(kern), smem, optin)) return rc;
-  const int64_t blocks = (rows + RG - 1) / RG, most = static_cast<int64_t>(sms) * fwd_blocks(TPR);
+  const int64_t blocks = (rows + RG - 1) / RG, most = static_cast<int64_t>(sms) * fwd_blocks<T>(TPR);
   return launch_k(kern, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
                   dim3(block_of<TPR>()), smem, st, 1, x, gamma, beta, rows, d, eps, y, mean, rstd);
 }

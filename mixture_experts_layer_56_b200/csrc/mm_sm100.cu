@@ -25,6 +25,15 @@
 // nobody owns, which may hold NaN).  MMA steps of 16 that hold none of the
 // group's rows are not issued, and warp 3 of each CTA zeroes the rest of the
 // last one in both operands in shared memory before the MMAs may read it.
+//
+// Bound by the tensor cores (full groups), whose rate under long loads is the
+// power cap's: 16 groups of 4096 rows of 2048 x 2048 forward 375 us, 1466
+// TFLOP/s (the library's best single product of 8192 cubed reaches 1643, and
+// 1369 in a loop); 63 groups of some 910 rows of 1792 x 1280 250 us, 1050
+// TFLOP/s, a last tile per group being part empty; the weight gradient at 1784 x
+// 1288 362 us, whose row pitches are no multiple of 128 bytes and cost the TMA
+// loads and L2 a third.  Bound by memory (few rows per group): 8 tokens x 6 of 64
+// experts of 2816 x 2048 63 us, 0.98 of the rate of a copy.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -231,6 +240,15 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     tmem_alloc_pair(smem_addr(&tmem_slot), TMEM_COLS);
     tmem_relinquish_pair();
   }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  tc_fence_before();
+  cluster_sync_all();  // barrier inits and TMEM allocations visible to the pair
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  // all of the above runs while the kernel before this one ends
   pdl_wait();
   pdl_trigger();
   if (RAG_M || RAG_K || RAG_N) {
@@ -272,11 +290,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       }
       if (lane == 0) tile_start[0] = 0;
     }
+    __syncthreads();
   }
-  tc_fence_before();
-  cluster_sync_all();  // barrier inits and TMEM allocations visible to the pair
-  tc_fence_after();
-  const uint32_t tmem_base = tmem_slot;
   const int mt_fixed = RAG_M ? 0 : (args.m + kTile - 1) / kTile;
   // a symmetric product's block of rows mb has the column tiles from its
   // diagonal block on, each 1 / per_blk of a block wide (above the diagonal,
@@ -370,11 +385,6 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
   if (warp == 0) {
     // ---------------------------------------------------- TMA producer ----
-    if (lane == 0) {
-      tma_prefetch_desc(&tmA);
-      tma_prefetch_desc(&tmB);
-    }
-    __syncwarp();
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_parity = 0;
     bool ok = true;

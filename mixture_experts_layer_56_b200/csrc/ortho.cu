@@ -20,6 +20,13 @@
 // X is held times a power of two near sqrt(max side), which centres its
 // entries in fp16's range.  A and B are symmetric: only the tiles on and above
 // the diagonal are computed, and written twice.
+//
+// Bound by the tensor cores and the power cap: 64 matrices of 2048 x 1408, five
+// steps, 4.79 TFLOP (symmetric halves counted once), 5.4 ms while the clock is at
+// 1.9 GHz, 6.4 when the cap holds it near 1.2 GHz; per step A takes 235 us, B 197
+// and the update 510 (it reads hi, lo and writes both beside its product, 1.5 GB).
+// Matrices of few hundred rows are bound by three launches a step of about 10 us
+// each: 5 x 640 x 560 155 us.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -8,6 +8,9 @@ Python side:
 * ``layer.MoELayer``: device weights, packed W13, workspace; ``forward`` runs
   ``moe_layer_forward`` on torch's current stream, ``forward_host`` runs
   ``moe_layer_forward_host`` on pinned host buffers.
+* ``training``: ``TrainableExperts`` (gate/up product, SwiGLU, down product and
+  their gradients over the rows of a dispatch), ``LayerNorm`` and
+  ``orthogonalize`` (the Muon optimiser's update of the stacked matrices).
 * ``synthetic``: seeded counter-based inputs of the benchmark workloads (no
   layer arithmetic).
 

@@ -26,7 +26,7 @@
 // 1.9 GHz, 6.4 when the cap holds it near 1.2 GHz; per step A takes 235 us, B 197
 // and the update 510 (it reads hi, lo and writes both beside its product, 1.5 GB).
 // Matrices of few hundred rows are bound by three launches a step of about 10 us
-// each: 5 x 640 x 560 155 us.
+// each: one of 256 x 256 108 us, five of 640 x 560 167.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -5,7 +5,8 @@
 // buffers: the next slice is on its way from global memory while one is
 // multiplied.  MI = 8 (128 x 128 tiles) reads 16 values from shared memory
 // per 64 multiply-adds and is bound by the fp32 pipe; MI = 4 (64 x 64 tiles)
-// is for shapes whose larger tiles would leave SMs idle or rows empty.
+// is for shapes whose larger tiles would leave SMs idle or rows empty.  Groups of
+// few rows have kernels of their own, which stream the matrices.
 // Multiply-adds are issued in pairs (fma.rn.f32x2, each lane rounded as an
 // fma.rn.f32).
 //
@@ -36,6 +37,39 @@ __device__ __forceinline__ F2 ld_cluster_f2(uint32_t addr) {
   F2 v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
   return v;
+}
+
+// tile_start[g + 1], the tiles of group g, become the number up to and with
+// group g.  Every thread of the block calls it, behind a barrier; it ends with
+// one.
+__device__ __forceinline__ void scan_tiles(int32_t* tile_start, int groups, int tid) {
+  if (tid < 32) {
+    // a run of groups per lane
+    const int per = (groups + 31) / 32, beg = min(tid * per, groups), end = min(beg + per, groups);
+    int sum = 0;
+    for (int i = beg; i < end; ++i) sum += tile_start[i + 1];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (tid >= o) incl += v;
+    }
+    int run = incl - sum;
+    for (int i = beg; i < end; ++i) {
+      run += tile_start[i + 1];
+      tile_start[i + 1] = run;
+    }
+    if (tid == 0) tile_start[0] = 0;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ int group_of_tile(const int32_t* tile_start, int groups, int tile) {
+  int lo = 0, hi = groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tile_start[mid] <= tile) lo = mid; else hi = mid - 1;
+  }
+  return lo;
 }
 
 // Four neighbours p[0..3], those at or past `left` zero.
@@ -123,36 +157,13 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
   for (int g = tid; g < groups; g += 256)
     tile_start[g + 1] = (DW ? mt_dw : (rowsg[g] + T - 1) / T) * nt;
   __syncthreads();
-  if (tid < 32) {
-    // inclusive scan, a run of groups per lane
-    const int per = (groups + 31) / 32, beg = min(tid * per, groups), end = min(beg + per, groups);
-    int sum = 0;
-    for (int i = beg; i < end; ++i) sum += tile_start[i + 1];
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (tid >= o) incl += v;
-    }
-    int run = incl - sum;
-    for (int i = beg; i < end; ++i) {
-      run += tile_start[i + 1];
-      tile_start[i + 1] = run;
-    }
-    if (tid == 0) tile_start[0] = 0;
-  }
-  __syncthreads();
+  scan_tiles(tile_start, groups, tid);
   const int total = tile_start[groups];
   const int tx = tid & 15, ty = tid >> 4;
   const int64_t lda = FWD ? k : n, ldb = k;
   const bool vec_a = lda % 4 == 0, vec_b = ldb % 4 == 0;
   for (int tile = blockIdx.x / parts; tile < total; tile += gridDim.x / parts) {
-    int lo = 0, hi = groups - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (tile_start[mid] <= tile) lo = mid; else hi = mid - 1;
-    }
-    const int g = lo;
+    const int g = group_of_tile(tile_start, groups, tile);
     const int local = tile - tile_start[g];
     const int m0 = (local / nt) * T, n0 = (local % nt) * T;
     const int64_t r0 = row0s[g];
@@ -256,6 +267,241 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
   }
 }
 
+// Few rows per group: the matrices are streamed once, up to kFewR rows of the
+// group with them, and bound by memory (40 groups of one row of 2392 x 1528:
+// forward 109 us, 5.4 TB/s, input gradient 139; in 64 x 64 tiles, almost all of
+// each of them empty, 594 and 694).
+constexpr int kFewR = 8;
+constexpr int kFewK = 1024;  // reduction steps of the rows in shared memory at a time
+
+// The tiles of kFewR rows by `blocks` of every group, and the groups' rows.
+__device__ __forceinline__ void few_tiles(const int32_t* offsets, int groups, int rows, int blocks,
+                                          int32_t* tile_start, int32_t* row0s, int32_t* rowsg,
+                                          int tid) {
+  group_spans(offsets, groups, rows, tile_start, tid, 256);
+  for (int g = tid; g < groups; g += 256) {
+    row0s[g] = tile_start[g];
+    rowsg[g] = tile_start[g + 1] - tile_start[g];
+  }
+  __syncthreads();
+  for (int g = tid; g < groups; g += 256)
+    tile_start[g + 1] = (rowsg[g] + kFewR - 1) / kFewR * blocks;
+  __syncthreads();
+  scan_tiles(tile_start, groups, tid);
+}
+
+// Forward: a warp takes four rows of W_g, its lanes along k, and R rows of the
+// group.  VEC: rows of whole 16-byte pieces, loaded without conditions, so that
+// they go out together.
+template <int R, bool VEC, typename Fill>
+__device__ __forceinline__ void few_dot(const float* w, int n, int k, int n0,
+                                        const float (*xs)[kFewK], Fill fill, int here, int lane,
+                                        float* y) {
+  const float* wr[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // past the last row: the last one, not stored
+    wr[i] = w + static_cast<int64_t>(min(n0 + i, n - 1)) * k;
+  F2 acc[4][R];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[i][r] = 0;
+  for (int k0 = 0; k0 < k; k0 += kFewK) {
+    const int len = min(kFewK, k - k0);
+    fill(k0, len);
+#pragma unroll(R > 2 ? 2 : 4)
+    for (int c = lane * 4; c < len; c += 128) {
+      F2 v[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* from = wr[i] + k0 + c;
+        const float4 f = VEC ? *reinterpret_cast<const float4*>(from) : load4(from, len - c, false);
+        v[i][0] = pair(f.x, f.y);
+        v[i][1] = pair(f.z, f.w);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&xs[r][c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][r] = fma2(v[i][1], x.y, fma2(v[i][0], x.x, acc[i][r]));
+      }
+    }
+  }
+  // 4 R sums over the lanes, of which lane l ends with number l % (4 R)
+  float v[4 * R];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float2 f = both(acc[i][r]);
+      v[i * R + r] = f.x + f.y;
+    }
+#pragma unroll
+  for (int o = 2 * R; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+#pragma unroll
+  for (int o = 4 * R; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  const int r = lane % R, c = n0 + lane / R;
+  if (lane < 4 * R && r < here && c < n) y[static_cast<int64_t>(r) * n + c] = v[0];
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(256, 2)
+grouped_f32_few_fwd_kernel(const float* __restrict__ x, const float* __restrict__ w,
+                           const int32_t* __restrict__ offsets, int groups, int rows, int n, int k,
+                           float* __restrict__ y) {
+  __shared__ __align__(16) float xs[kFewR][kFewK];
+  __shared__ int32_t tile_start[kMaxG + 1], row0s[kMaxG], rowsg[kMaxG];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nb = (n + 31) / 32;
+  few_tiles(offsets, groups, rows, nb, tile_start, row0s, rowsg, tid);
+  const int64_t total = tile_start[groups];
+  // a run of tiles, so that most of them find their rows in place
+  const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+  int64_t in_place = -1;  // first row of what xs holds
+  for (int tile = static_cast<int>(total * blockIdx.x / gridDim.x); tile < end; ++tile) {
+    const int g = group_of_tile(tile_start, groups, tile);
+    const int local = tile - tile_start[g], chunk = local / nb;
+    const int n0 = (local - chunk * nb) * 32 + warp * 4;
+    const int64_t r0 = static_cast<int64_t>(row0s[g]) + chunk * kFewR;
+    const int here = min(kFewR, rowsg[g] - chunk * kFewR);
+    auto fill = [&](int k0, int len) {
+      if (k <= kFewK && in_place == r0) return;
+      __syncthreads();  // what xs held has been used
+      for (int e = tid; e < here * (kFewK / 4); e += 256) {
+        const int r = e / (kFewK / 4), c = e % (kFewK / 4) * 4;
+        if (c < len)
+          *reinterpret_cast<float4*>(&xs[r][c]) = load4(x + (r0 + r) * k + k0 + c, len - c, VEC);
+      }
+      __syncthreads();
+      in_place = r0;
+    };
+    const float* wg = w + static_cast<int64_t>(g) * n * k;
+    float* to = y + r0 * n;
+    if (here == 1) few_dot<1, VEC>(wg, n, k, n0, xs, fill, here, lane, to);
+    else if (here == 2) few_dot<2, VEC>(wg, n, k, n0, xs, fill, here, lane, to);
+    else if (here <= 4) few_dot<4, VEC>(wg, n, k, n0, xs, fill, here, lane, to);
+    else few_dot<kFewR, VEC>(wg, n, k, n0, xs, fill, here, lane, to);
+  }
+}
+
+// Input gradient: a lane takes four columns of W_g, the block's warps its rows
+// in turn.  The CTAs of a cluster take a part of the rows each.
+template <int R, bool VEC>
+__device__ __forceinline__ void few_axpy(const float* wc, int64_t ld, int left,
+                                         const float (*ds)[kFewR], int len, int warp,
+                                         F2 (&acc)[kFewR][2]) {
+#pragma unroll 8
+  for (int j = warp; j < len; j += 8) {
+    const float4 v = VEC ? *reinterpret_cast<const float4*>(wc + j * ld) : load4(wc + j * ld, left, false);
+    const F2 w0 = pair(v.x, v.y), w1 = pair(v.z, v.w);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const F2 d = pair(ds[j][r], ds[j][r]);
+      acc[r][0] = fma2(d, w0, acc[r][0]);
+      acc[r][1] = fma2(d, w1, acc[r][1]);
+    }
+  }
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(256, 2)
+grouped_f32_few_dx_kernel(const float* __restrict__ dy, const float* __restrict__ w,
+                          const int32_t* __restrict__ offsets, int groups, int rows, int n, int k,
+                          float* __restrict__ dx) {
+  // the rows' slice, then the warps' sums, then in warp 0's place the block's
+  __shared__ __align__(16) float buf[8][kFewR][128];
+  static_assert(sizeof(buf) >= kFewK * kFewR * 4, "the slice takes the sums' place");
+  float (*const ds)[kFewR] = reinterpret_cast<float (*)[kFewR]>(&buf[0][0][0]);
+  __shared__ int32_t tile_start[kMaxG + 1], row0s[kMaxG], rowsg[kMaxG];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int part = static_cast<int>(cluster_ctarank());
+  const int parts = static_cast<int>(gridDim.x / num_clusters_x());
+  const int per = (n + parts - 1) / parts;
+  const int nbeg = min(part * per, n), nend = min(nbeg + per, n);
+  const int kb = (k + 127) / 128;
+  few_tiles(offsets, groups, rows, kb, tile_start, row0s, rowsg, tid);
+  const int total = tile_start[groups];
+  for (int tile = blockIdx.x / parts; tile < total; tile += gridDim.x / parts) {
+    const int g = group_of_tile(tile_start, groups, tile);
+    const int local = tile - tile_start[g], chunk = local / kb;
+    const int c0 = (local - chunk * kb) * 128 + lane * 4;
+    const int64_t r0 = static_cast<int64_t>(row0s[g]) + chunk * kFewR;
+    const int here = min(kFewR, rowsg[g] - chunk * kFewR);
+    // VEC: lanes past the row take its first columns, which they do not store
+    const float* wg = w + static_cast<int64_t>(g) * n * k + (VEC && c0 >= k ? 0 : c0);
+    F2 acc[kFewR][2];
+#pragma unroll
+    for (int r = 0; r < kFewR; ++r) acc[r][0] = acc[r][1] = 0;
+    for (int j0 = nbeg; j0 < nend; j0 += kFewK) {
+      const int len = min(kFewK, nend - j0);
+      __syncthreads();  // what was in the buffer has been used
+      for (int e = tid; e < here * kFewK; e += 256) {
+        const int r = e / kFewK, j = e % kFewK;
+        if (j < len) ds[j][r] = dy[(r0 + r) * n + j0 + j];
+      }
+      __syncthreads();
+      const float* wc = wg + static_cast<int64_t>(j0) * k;
+      if (here == 1) few_axpy<1, VEC>(wc, k, k - c0, ds, len, warp, acc);
+      else if (here == 2) few_axpy<2, VEC>(wc, k, k - c0, ds, len, warp, acc);
+      else if (here <= 4) few_axpy<4, VEC>(wc, k, k - c0, ds, len, warp, acc);
+      else few_axpy<kFewR, VEC>(wc, k, k - c0, ds, len, warp, acc);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kFewR; ++r)
+      *reinterpret_cast<ulonglong2*>(&buf[warp][r][lane * 4]) = make_ulonglong2(acc[r][0], acc[r][1]);
+    __syncthreads();
+    // warp r adds row r up, over the warps and then over the cluster, in order
+    float4 s = *reinterpret_cast<const float4*>(&buf[0][warp][lane * 4]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(&buf[i][warp][lane * 4]);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    if (parts > 1) {
+      *reinterpret_cast<float4*>(&buf[0][warp][lane * 4]) = s;
+      cluster_sync_all();
+      const uint32_t at = smem_addr(&buf[0][warp][lane * 4]);
+      if (warp % parts == part) {
+        F2 a = 0, b = 0;
+        for (int p = 0; p < parts; ++p) {
+          const uint32_t from = map_to_cta(at, static_cast<uint32_t>(p));
+          a = add2(a, ld_cluster_f2(from));
+          b = add2(b, ld_cluster_f2(from + 8));
+        }
+        const float2 lo = both(a), hi = both(b);
+        s = make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
+    }
+    if (warp < here && warp % parts == part) {
+      float* to = dx + (r0 + warp) * k + c0;
+      if (VEC) {
+        if (c0 < k) *reinterpret_cast<float4*>(to) = s;
+      } else {
+        if (c0 < k) to[0] = s.x;
+        if (c0 + 1 < k) to[1] = s.y;
+        if (c0 + 2 < k) to[2] = s.z;
+        if (c0 + 3 < k) to[3] = s.w;
+      }
+    }
+    if (parts > 1) cluster_sync_all();  // the sums have been read
+  }
+}
+
 template <int MI, bool SPLIT>
 int launch_tiles(int dir, const float* a, const float* b, const int32_t* offsets, int groups,
                  int64_t rows, int n, int k, float* out, bool accumulate, int64_t tiles, int most,
@@ -276,6 +522,24 @@ int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* o
                        cudaStream_t st) {
   const int64_t N = dir == kGroupedFwd ? n : k;
   const int64_t some = rows < groups ? rows : groups;  // groups with rows, at most
+  // Few rows per group, on average (16 groups of 2048 x 1024 forward, 24 rows: 95
+  // us for 145 in tiles, 40 rows: 154 for 147; input gradient, 24: 88 for 143, 40:
+  // 145 for 145).
+  if (dir != kGroupedDw && rows <= (dir == kGroupedFwd ? 24ll : 32ll) * groups) {
+    const int64_t blocks = (N + (dir == kGroupedFwd ? 31 : 127)) / (dir == kGroupedFwd ? 32 : 128);
+    const int64_t most = blocks * (rows / kFewR + some);
+    int parts = 1;
+    if (dir == kGroupedDx)
+      while (parts < 8 && most * parts < 4ll * sms && n >= 128 * parts) parts *= 2;
+    const int64_t fit = 2ll * sms / parts;
+    const int grid = static_cast<int>(most < fit ? most : fit) * parts;
+    auto kern = dir == kGroupedFwd ? (k % 4 == 0 ? grouped_f32_few_fwd_kernel<true>
+                                                 : grouped_f32_few_fwd_kernel<false>)
+                                   : (k % 4 == 0 ? grouped_f32_few_dx_kernel<true>
+                                                 : grouped_f32_few_dx_kernel<false>);
+    return launch_k(kern, dim3(grid), dim3(256), 0, st, parts, a, b, offsets, groups,
+                    static_cast<int>(rows), n, k, out);
+  }
   auto tiles = [&](int T) {
     const int64_t nt = (N + T - 1) / T;
     return nt * (dir == kGroupedDw ? static_cast<int64_t>(groups) * ((n + T - 1) / T)

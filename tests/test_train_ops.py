@@ -274,6 +274,14 @@ def test_grouped_f32_few_tiles_and_long_sums(sizes, n, k):
     run_grouped(sizes, n, k, torch.float32, lead=1, tail=2)
 
 
+@pytest.mark.parametrize("n,k", [(1, 1), (33, 130), (70, 1025), (2500, 128), (1030, 260), (513, 2047)])
+@pytest.mark.parametrize("sizes", [[1], [2, 0, 3], [8], [9, 1, 0, 4], [1] * 40, [0] * 30 + [50, 5],
+                                   [0] * 7 + [17]])
+def test_grouped_f32_few_rows(sizes, n, k):
+    """Groups of few rows on average, whose matrices are streamed."""
+    run_grouped(sizes, n, k, torch.float32, lead=3, tail=2, seed=n + len(sizes), dirs=("fwd", "dx"))
+
+
 # ------------------------------------------------------------------- SwiGLU
 def swiglu_ref(gu, da):
     b = gu.double().view(gu.shape[0], -1, 2, 64)

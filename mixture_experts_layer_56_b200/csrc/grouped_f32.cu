@@ -240,12 +240,32 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
       if (c < N) row[c] = accumulate ? row[c] + v.x : v.x;
       if (c + 1 < N) row[c + 1] = accumulate ? row[c + 1] + v.y : v.y;
     };
+    // dW: four neighbours in one store where rows are whole 16-byte pieces (the
+    // other two, whose outputs are few beside their reductions, lose registers)
+    auto store4 = [&](int i, int j, F2 lo, F2 hi) {
+      if (N % 4 != 0 || accumulate) {
+        store(i, j, lo);
+        store(i, j + 1, hi);
+        return;
+      }
+      const int m = m0 + (i >> 2) * 64 + ty * 4 + (i & 3), c = n0 + (j >> 1) * 64 + tx * 4;
+      if (m >= M || c >= N) return;
+      const float2 v = both(lo), w = both(hi);
+      *reinterpret_cast<float4*>(out + (static_cast<int64_t>(g) * n + m) * k + c) =
+          make_float4(v.x, v.y, w.x, w.y);
+    };
     if (!SPLIT) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < MI / 2; ++j)
-          store(i, j, DW ? add2(sum[i][j], acc[i][j]) : acc[i][j]);
+        for (int j = 0; j < MI / 2; ++j) {
+          if (!DW) {
+            store(i, j, acc[i][j]);
+          } else {
+            acc[i][j] = add2(sum[i][j], acc[i][j]);
+            if (j & 1) store4(i, j - 1, acc[i][j - 1], acc[i][j]);
+          }
+        }
     } else {
       // the CTAs' sums are added up in order, each CTA its share of the tile
       F2* mine = reinterpret_cast<F2*>(&slices[0][0][0]);
@@ -502,6 +522,78 @@ grouped_f32_few_dx_kernel(const float* __restrict__ dy, const float* __restrict_
   }
 }
 
+// Weight gradient: a lane takes four columns of dW_g, the block's warps its rows
+// in turn, kFewN of them a tile; bound by the writes (40 groups of one row of
+// 2392 x 1528: 95 us, 6.1 TB/s; in 64 x 64 tiles 308).
+constexpr int kFewN = 128;
+
+template <bool VEC>
+__global__ void __launch_bounds__(256, 3)
+grouped_f32_few_dw_kernel(const float* __restrict__ dy, const float* __restrict__ x,
+                          const int32_t* __restrict__ offsets, int groups, int rows, int n, int k,
+                          float* __restrict__ dw, bool accumulate) {
+  __shared__ __align__(16) float ds[kFewN][kFewR];
+  __shared__ int32_t span[kMaxG + 1];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  group_spans(offsets, groups, rows, span, tid, 256);
+  const int kb = (k + 127) / 128, nb = (n + kFewN - 1) / kFewN;
+  const int64_t total = static_cast<int64_t>(groups) * kb * nb;
+  for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    const int g = static_cast<int>(tile / (kb * nb)), local = static_cast<int>(tile % (kb * nb));
+    const int n0 = local / kb * kFewN, c0 = local % kb * 128 + lane * 4;
+    const int left = min(kFewN, n - n0);
+    const int64_t r0 = span[g];
+    const int len = span[g + 1] - span[g];
+    float* to = dw + (static_cast<int64_t>(g) * n + n0) * k + c0;
+    // more rows than kFewR are added in turn to what lies there
+    bool add = accumulate;
+    for (int c = 0; c < max(len, add ? 0 : 1); c += kFewR, add = true) {
+      const int here = min(kFewR, len - c);
+      __syncthreads();  // the slice before has been used
+      for (int e = tid; e < kFewR * kFewN; e += 256) {
+        const int r = e / kFewN, j = e % kFewN;
+        ds[j][r] = r < here && j < left ? dy[(r0 + c + r) * n + n0 + j] : 0.0f;
+      }
+      F2 v[kFewR][2];
+#pragma unroll
+      for (int r = 0; r < kFewR; ++r) {
+        float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < here) f = load4(x + (r0 + c + r) * k + c0, k - c0, VEC);
+        v[r][0] = pair(f.x, f.y);
+        v[r][1] = pair(f.z, f.w);
+      }
+      __syncthreads();
+#pragma unroll 2
+      for (int j = warp; j < left; j += 8) {
+        float* at = to + static_cast<int64_t>(j) * k;
+        F2 s0 = 0, s1 = 0;
+#pragma unroll
+        for (int r = 0; r < kFewR; ++r) {
+          const F2 d = pair(ds[j][r], ds[j][r]);
+          s0 = fma2(d, v[r][0], s0);
+          s1 = fma2(d, v[r][1], s1);
+        }
+        if (add) {
+          const float4 f = load4(at, k - c0, VEC);
+          s0 = add2(s0, pair(f.x, f.y));
+          s1 = add2(s1, pair(f.z, f.w));
+        }
+        const float2 lo = both(s0), hi = both(s1);
+        if (VEC) {
+          if (c0 < k) *reinterpret_cast<float4*>(at) = make_float4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+          if (c0 < k) at[0] = lo.x;
+          if (c0 + 1 < k) at[1] = lo.y;
+          if (c0 + 2 < k) at[2] = hi.x;
+          if (c0 + 3 < k) at[3] = hi.y;
+        }
+      }
+    }
+  }
+}
+
 template <int MI, bool SPLIT>
 int launch_tiles(int dir, const float* a, const float* b, const int32_t* offsets, int groups,
                  int64_t rows, int n, int k, float* out, bool accumulate, int64_t tiles, int most,
@@ -539,6 +631,13 @@ int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* o
                                                  : grouped_f32_few_dx_kernel<false>);
     return launch_k(kern, dim3(grid), dim3(256), 0, st, parts, a, b, offsets, groups,
                     static_cast<int>(rows), n, k, out);
+  }
+  // (the same, 8 rows: 33 us for 56; 16 rows: 66 for 57)
+  if (dir == kGroupedDw && rows <= 8ll * groups) {
+    const int64_t most = static_cast<int64_t>(groups) * ((k + 127) / 128) * ((n + kFewN - 1) / kFewN);
+    auto kern = k % 4 == 0 ? grouped_f32_few_dw_kernel<true> : grouped_f32_few_dw_kernel<false>;
+    return launch_k(kern, dim3(static_cast<unsigned>(most < 3ll * sms ? most : 3ll * sms)), dim3(256),
+                    0, st, 1, a, b, offsets, groups, static_cast<int>(rows), n, k, out, accumulate);
   }
   auto tiles = [&](int T) {
     const int64_t nt = (N + T - 1) / T;

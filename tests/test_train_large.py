@@ -118,6 +118,24 @@ def test_grouped_f32():
         close(y[r], x[r].double() @ wg, (k + 2) * U * (x[r].double().abs() @ wg.abs()))
 
 
+def test_grouped_f32_few_rows():
+    groups, n, k = 66, 8192, 4104
+    w = rnd(groups, n, k).float()
+    x, dy = rnd(groups, k).float(), rnd(groups, n).float()
+    off = torch.arange(groups + 1, device="cuda").int()
+    shape = L.make_grouped_shape(groups, groups, n, k, L.MOE_DTYPE_F32)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    y, dx, dw = torch.empty_like(dy), torch.empty_like(x), torch.empty_like(w)
+    L.moe_grouped_matmul(shape, x, off, w, y, ws)
+    L.moe_grouped_matmul_dx(shape, dy, off, w, dx, ws)
+    L.moe_grouped_matmul_dw(shape, dy, x, off, dw, ws)
+    for g in spots(groups, n * k):
+        wg, xg, dg = w[g].double(), x[g].double(), dy[g].double()
+        close(y[g], wg @ xg, (k + 2) * U * (wg.abs() @ xg.abs()))
+        close(dx[g], dg @ wg, (n + 2) * U * (dg.abs() @ wg.abs()))
+        close(dw[g], torch.outer(dg, xg), 2 * U * torch.outer(dg, xg).abs())
+
+
 def test_swiglu():
     rows, inter = 300000, 4096  # gu passes 2^31 elements, and 2^32 bytes
     gu, da = rnd(rows, 2 * inter), rnd(rows, inter)

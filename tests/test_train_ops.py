@@ -279,7 +279,31 @@ def test_grouped_f32_few_tiles_and_long_sums(sizes, n, k):
                                    [0] * 7 + [17]])
 def test_grouped_f32_few_rows(sizes, n, k):
     """Groups of few rows on average, whose matrices are streamed."""
-    run_grouped(sizes, n, k, torch.float32, lead=3, tail=2, seed=n + len(sizes), dirs=("fwd", "dx"))
+    run_grouped(sizes, n, k, torch.float32, lead=3, tail=2, seed=n + len(sizes))
+
+
+def test_grouped_f32_few_rows_accumulate():
+    """Onto what is there, a group of more rows than are added at once and
+    empty ones among them."""
+    g = gen(8)
+    sizes, n, k = [0, 1, 21, 0, 8, 2], 150, 262
+    off = torch.tensor([0] + sizes).cumsum(0).int().cuda()
+    x, dy = randn(g, sum(sizes), k), randn(g, sum(sizes), n)
+    dw = randn(g, len(sizes), n, k)
+    before = dw.clone()
+    shape = L.make_grouped_shape(sum(sizes), len(sizes), n, k, L.MOE_DTYPE_F32,
+                                 L.MOE_GROUPED_DW_ACCUMULATE)
+    ws = clear_status(scratch(L.moe_grouped_workspace_size(shape)))
+    L.moe_grouped_matmul_dw(shape, dy, x, off, dw, ws)
+    for e in range(len(sizes)):
+        a, b = int(off[e]), int(off[e + 1])
+        ref, tol = group_tol(dy[a:b].double().T, x[a:b].double(), b - a, torch.float32, torch.float32)
+        full = ref + before[e].double()
+        # each of the three additions onto the sum rounds once
+        assert_close(dw[e], full, tol + 3 * U * (before[e].double().abs() + dy[a:b].double().abs().T
+                                                 @ x[a:b].double().abs()), e)
+        if a == b:
+            assert torch.equal(dw[e], before[e])
 
 
 # ------------------------------------------------------------------- SwiGLU

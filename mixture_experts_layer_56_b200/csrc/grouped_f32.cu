@@ -14,7 +14,7 @@
 // a time and adds these sums up apart, which keeps the rounding of long groups
 // near sqrt(128) rather than sqrt(rows) half steps.  The other two sum a
 // matrix's width in one chain, as two blocks per SM leave no registers for
-// more (8 x 1024 x 2048 x 1024: 49 TFLOP/s, with apart sums 46).
+// more (8 x 1024 x 2048 x 1024: 54 TFLOP/s; with apart sums 6% less).
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -645,15 +645,17 @@ int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* o
                                    : (rows + T - 1) / T + some);
   };
   // The tile size whose most loaded SM is done first: a 128 x 128 tile is four
-  // 64 x 64 ones, which take 1.45 times as long for the same work (8 x 1024 x
-  // 2048 x 1024: 49 against 34 TFLOP/s; 16 x 300 x 512 x 512: 105 against 93 us).
+  // 64 x 64 ones, which take some 1.45 times as long for the same work (8 x 1024 x
+  // 2048 x 1024: forward 633 against 1015 us, dX 758 and 976, dW 689 and 968; 16 x
+  // 300 x 512 x 512, part empty in the large ones: 96 against 93, 100 and 91, 64
+  // and 86).
   auto rounds = [&](int T) { return (tiles(T) + sms - 1) / sms; };
   const bool fill = dir == kGroupedDw || rows >= 96 * some;  // groups fill the large ones
   if (fill && 4.0 * rounds(128) <= 1.45 * rounds(64))
     return launch_tiles<8, false>(dir, a, b, offsets, groups, rows, n, k, out, accumulate,
                                   tiles(128), dir == kGroupedDw ? sms : 2 * sms, 1, st);
   // Few tiles: clusters of up to 8 CTAs share a tile's reduction, four slices
-  // each at least (6 x 357 rows of 248 x 656: 46 us without).
+  // each at least (6 x 357 rows of 248 x 656 forward: 30 us, without 46).
   const int64_t length = dir == kGroupedFwd ? k : dir == kGroupedDx ? n : rows / groups;
   int parts = 1;
   while (parts < 8 && tiles(64) * parts * 2 <= 4ll * sms && length >= 4ll * TK * parts * 2) parts *= 2;

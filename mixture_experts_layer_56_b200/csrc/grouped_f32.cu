@@ -289,7 +289,7 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
 
 // Few rows per group: the matrices are streamed once, up to kFewR rows of the
 // group with them, and bound by memory (40 groups of one row of 2392 x 1528:
-// forward 109 us, 5.4 TB/s, input gradient 139; in 64 x 64 tiles, almost all of
+// forward 109 us, 5.4 TB/s, input gradient 121; in 64 x 64 tiles, almost all of
 // each of them empty, 594 and 694).
 constexpr int kFewR = 8;
 constexpr int kFewK = 1024;  // reduction steps of the rows in shared memory at a time
@@ -622,7 +622,7 @@ int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* o
     const int64_t most = blocks * (rows / kFewR + some);
     int parts = 1;
     if (dir == kGroupedDx)
-      while (parts < 8 && most * parts < 4ll * sms && n >= 128 * parts) parts *= 2;
+      while (parts < 8 && most * parts < 2ll * sms && n >= 128 * parts) parts *= 2;
     const int64_t fit = 2ll * sms / parts;
     const int grid = static_cast<int>(most < fit ? most : fit) * parts;
     auto kern = dir == kGroupedFwd ? (k % 4 == 0 ? grouped_f32_few_fwd_kernel<true>

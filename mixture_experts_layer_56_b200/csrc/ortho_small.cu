@@ -50,6 +50,13 @@ __device__ __forceinline__ uint32_t cluster_size_x() {
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
   return r;
 }
+// cluster_sync_all in two halves, for the work of one CTA between them
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -119,6 +126,10 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
     tmem_alloc(smem_addr(&tmem_slot), 512);
     tmem_relinquish();
   }
+  // A CTA's shared memory may be written from the others only once it has
+  // started: they wait for that behind the pass over M.
+  __syncwarp();
+  cluster_arrive();
   pdl_wait();
   pdl_trigger();
 
@@ -178,6 +189,7 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) red[warp] = s;
   __syncthreads();
+  cluster_wait();  // every CTA has started
   if (tid < size) {
     double t = 0.0;
 #pragma unroll

@@ -1,0 +1,57 @@
+"""Calls of the training operators that a program makes beside the plain ones:
+several at once, stacks past what the GPU holds, large gradients, infinities."""
+import pytest
+import torch
+
+from mixture_experts_layer_56_b200 import _lib as L
+
+pytestmark = pytest.mark.gpu
+
+DT = {torch.float32: L.MOE_DTYPE_F32, torch.bfloat16: L.MOE_DTYPE_BF16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    yield
+
+
+def randn(seed, *shape, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, device="cuda", generator=g).to(dtype)
+
+
+def ortho_call(m, o, steps=5):
+    n, r, c = m.shape
+    shape = L.make_ortho_shape(n, r, c, steps, DT[m.dtype])
+    ws = torch.zeros(max(256, L.moe_orthogonalize_workspace_size(shape)), dtype=torch.uint8,
+                     device="cuda")
+    return lambda stream=None: L.moe_orthogonalize(shape, m, o, ws, stream=stream), ws
+
+
+@pytest.mark.parametrize("r,c", [(64, 330), (1100, 40), (128, 2048)])
+def test_orthogonalize_more_clusters_than_fit(r, c):
+    """Clusters that start late, beside one another and behind other work, some
+    of whose CTAs own no column (330 of 512): each matrix comes out as alone."""
+    m = randn(r, 150, r, c)
+    outs = [torch.empty(m.shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    calls = [ortho_call(m, o) for o in outs]
+    streams = [torch.cuda.Stream() for _ in calls]
+    big = randn(1, 4096, 4096)
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for (call, _), s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                big @ big
+            call(stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1])
+    for i in (0, 77, 149):
+        one = torch.empty(1, r, c, dtype=torch.bfloat16, device="cuda")
+        ortho_call(m[i:i + 1].contiguous(), one)[0]()
+        assert torch.equal(one[0], outs[0][i])
+    assert [L.moe_read_status(ws) for _, ws in calls] == [0, 0]

@@ -282,6 +282,7 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
         for (int p = 0; p < parts; ++p) v = add2(v, ld_cluster_f2(map_to_cta(at, p)));
         store(e / (MI / 2), e % (MI / 2), v);
       }
+      __syncwarp();
       cluster_sync_all();
     }
   }
@@ -518,6 +519,7 @@ grouped_f32_few_dx_kernel(const float* __restrict__ dy, const float* __restrict_
         if (c0 + 3 < k) to[3] = s.w;
       }
     }
+    __syncwarp();
     if (parts > 1) cluster_sync_all();  // the sums have been read
   }
 }

@@ -244,6 +244,7 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
+  __syncwarp();
   tc_fence_before();
   cluster_sync_all();  // barrier inits and TMEM allocations visible to the pair
   tc_fence_after();
@@ -526,7 +527,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       if ((ti.rows & 15) != 0) {
         const int rem = ti.rows & (kKB - 1);
         const int s = (done + ti.nkb - 1) % STAGES;
-        if (!wait_bounded(land_bar(s), (parity >> s) & 1u, abort_p, args.status)) break;
+        if (!__all_sync(0xffffffffu,
+                        wait_bounded(land_bar(s), (parity >> s) & 1u, abort_p, args.status)))
+          break;
         parity ^= 1u << s;
         uint8_t* base = smem + s * STAGE_BYTES;
         // the rows from rem to the end of their step of 16 (the steps behind it
@@ -620,9 +623,9 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       // and results crossing instead cost 5 x 0.2 ms more at 64 x 2048 x 1408)
       auto stage_acc = [&](uint32_t addr) {
         float x[32];
+        __syncwarp();  // lanes leave the chunk before this one at different points
         tmem_ld32(addr, x);
         tmem_ld_wait_regs(x);
-        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           *reinterpret_cast<float4*>(stage + lane * kStagePitch + i * 16) =
@@ -653,7 +656,8 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const uint32_t ap = (it >> 1) & 1;
       if (!empty) {
         ++it;
-        if (!wait_bounded(tfull_bar(acc), ap, abort_p, args.status)) break;
+        if (!__all_sync(0xffffffffu, wait_bounded(tfull_bar(acc), ap, abort_p, args.status)))
+          break;
         tc_fence_after();
       }
       const int row = ti.m_blk * kTile + static_cast<int>(rank) * kHalf + r;

@@ -193,7 +193,10 @@ template <typename T> constexpr int bwd_blocks(int tpr) {
 template <int TPR>
 __device__ __forceinline__ void group_sync() {
   if (block_of<TPR>() == TPR) __syncthreads();
-  else asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / TPR), "n"(TPR) : "memory");
+  else {
+    __syncwarp();  // the barrier takes whole warps
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / TPR), "n"(TPR) : "memory");
+  }
 }
 
 // Rows on their way from memory: kRing rows per group, of each of the ARRAYS

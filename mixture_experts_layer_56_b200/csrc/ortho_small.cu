@@ -122,13 +122,13 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
     fence_mbar_init();
     fence_async_shared();
   }
+  __syncwarp();  // here and below: what is .aligned wants the warp's lanes together
   if (warp == 0) {
     tmem_alloc(smem_addr(&tmem_slot), 512);
     tmem_relinquish();
   }
   // A CTA's shared memory may be written from the others only once it has
   // started: they wait for that behind the pass over M.
-  __syncwarp();
   cluster_arrive();
   pdl_wait();
   pdl_trigger();
@@ -196,6 +196,7 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
     for (int i = 0; i < kSmThreads / 32; ++i) t += red[i];
     st_cluster_f64(map_to_cta(smem_addr(&sums[rank]), static_cast<uint32_t>(tid)), t);
   }
+  __syncwarp();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -236,6 +237,7 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
   auto wait_mma = [&] {
     wait_bounded(bar, phase, abort_p, status);
     phase ^= 1u;
+    __syncwarp();
     tc_fence_after();
   };
 
@@ -342,6 +344,7 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
         }
       }
       fence_async_cluster();
+      __syncwarp();
       cluster_sync_all();
     }
     // ---- 3. B = b A + c A A -------------------------------------------------
@@ -465,6 +468,7 @@ ortho_small_kernel(const T* __restrict__ M, bf16* __restrict__ O, int rows, int 
                    : static_cast<int64_t>(i) * cols + j + e] = __float2bfloat16_rn(v[e]);
     }
   }
+  __syncwarp();
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -61,6 +61,7 @@ constexpr int kStagePitch = 128 + 16;  // staging row: 128 bytes, padded off the
 constexpr int kWarpStage = 32 * kStagePitch;
 constexpr int kWarpDiag = 128 * 4;  // a diagonal's values over an epilogue warp's columns
 constexpr uint32_t kSliceBytes = 64 * kKB * 2;  // an MN-major 64-wide slice
+constexpr uint64_t kLandNs = 1000000;  // copies in flight after an expired wait: 1 ms
 constexpr int kColChunk = 8;  // N tiles that a group's row blocks sweep together
 
 // Shared memory with BR rows of B per CTA in a stage.
@@ -456,6 +457,12 @@ mm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           int dummy = 0;
           wait_bounded(empty_bar(s), (issued_parity >> s) & 1u, &dummy, nullptr);
         }
+    } else {
+      // A wait ran out.  Copies that were issued land in microseconds, on
+      // barriers that may be the other CTA's; this CTA's memory stays until then.
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < kLandNs) {
+      }
     }
     __syncwarp();
   } else if (warp == 1) {

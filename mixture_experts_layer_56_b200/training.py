@@ -112,29 +112,35 @@ class TrainableExperts:
 
     def backward(self, dy: torch.Tensor, stream=None) -> torch.Tensor:
         """The gradient of ``forward``'s x from that of its y; adds to dW13 and
-        dW2.  Once per forward."""
+        dW2.  Once per forward.  A refusal or a lack of memory leaves the
+        forward and the gradients as they are; an error after dW2 was issued
+        leaves the two apart, and the next call asks for ``zero_grad``."""
         if self._saved is None:
             raise RuntimeError("backward() without a forward() before it")
         x, offsets, gu, a, saved_on = self._saved
         if self._rows(dy, self.d, "dy").shape != x.shape:
             raise ValueError("dy has to have as many rows as x")
         _same_stream(saved_on, stream)
-        self._saved = None
+        if self._have_grad is None:
+            raise RuntimeError("an earlier backward() failed between dW2 and dW13: zero_grad() first")
         rows, flags = x.shape[0], L.MOE_GROUPED_DW_F32
         if self._have_grad:
             flags |= L.MOE_GROUPED_DW_ACCUMULATE
-        self._have_grad = True
         up = self._shape(rows, 2 * self.inter, self.d, flags)
         down = self._shape(rows, self.d, self.inter, flags)
         with _on(stream):
             da, dx = torch.empty_like(a), torch.empty_like(x)
+        # up to here an error changes nothing
+        self._saved = None
         L.moe_grouped_matmul_dx(down, dy, offsets, self.W2, da, self.ws, stream=stream)
         L.moe_grouped_matmul_dw(down, dy, a, offsets, self.dW2, self.ws, stream=stream)
+        self._have_grad = None  # until dW13 has what dW2 has
         # the pre-activations' gradient takes their place
         L.moe_swiglu_backward(L.make_swiglu_shape(rows, self.inter, _DTYPE[self.dtype]), gu, da, gu,
                               stream=stream)
         L.moe_grouped_matmul_dx(up, gu, offsets, self.W13, dx, self.ws, stream=stream)
         L.moe_grouped_matmul_dw(up, gu, x, offsets, self.dW13, self.ws, stream=stream)
+        self._have_grad = True
         return dx
 
     def zero_grad(self):

@@ -1,0 +1,112 @@
+"""training.py's bookkeeping: what a call keeps, and leaves behind when it
+fails.  The library's entries are replaced by ones that record their calls; no
+GPU."""
+import pytest
+import torch
+
+from mixture_experts_layer_56_b200 import _lib as L
+from mixture_experts_layer_56_b200 import training as TR
+
+ENTRIES = ("moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw", "moe_swiglu",
+           "moe_swiglu_backward", "moe_layer_norm", "moe_layer_norm_backward", "moe_orthogonalize")
+STREAM = 4321
+
+
+class Calls(list):
+    """(entry, arguments, stream) of each call; `fail` names the entry whose
+    n-th call from now raises."""
+    fail = None
+
+    def entry(self, name):
+        def call(*args, stream=None, **kw):
+            if self.fail is not None and self.fail[0] == name:
+                self.fail = (name, self.fail[1] - 1) if self.fail[1] > 1 else None
+                if self.fail is None:
+                    raise L.MoeError(name, L.MOE_ERR_CUDA)
+            self.append((name, args, stream))
+        return call
+
+    def named(self, name):
+        return [args for n, args, _ in self if n == name]
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    seen = Calls()
+    for name in ENTRIES:
+        monkeypatch.setattr(L, name, seen.entry(name))
+    for name in ("moe_layer_norm_workspace_size", "moe_orthogonalize_workspace_size"):
+        monkeypatch.setattr(L, name, lambda shape: 1 << 16)
+    monkeypatch.setattr(L, "_stream", lambda stream: STREAM if stream is None else stream)
+    monkeypatch.setattr(TR, "_on_current", lambda t, what: t)
+    return seen
+
+
+def experts():
+    return TR.TrainableExperts(torch.ones(2, 128, 16), torch.ones(2, 16, 64))
+
+
+def flags(calls):
+    return [a[0].flags for a in calls.named("moe_grouped_matmul_dw")]
+
+
+OFF = torch.tensor([0, 2, 4], dtype=torch.int32)
+OVER, ADD = L.MOE_GROUPED_DW_F32, L.MOE_GROUPED_DW_F32 | L.MOE_GROUPED_DW_ACCUMULATE
+
+
+def no_memory(*a, **kw):
+    raise torch.OutOfMemoryError("planted")
+
+
+def test_backward_without_memory_changes_nothing(calls, monkeypatch):
+    ex, x = experts(), torch.ones(4, 16)
+    ex.forward(x, OFF)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "empty_like", no_memory)
+        with pytest.raises(torch.OutOfMemoryError):
+            ex.backward(x)
+    assert not calls.named("moe_grouped_matmul_dw")
+    ex.backward(x)              # the forward is still there
+    assert flags(calls) == [OVER, OVER]
+    ex.forward(x, OFF)
+    ex.backward(x)
+    assert flags(calls)[2:] == [ADD, ADD]
+
+
+def test_backward_that_fails_before_a_gradient_keeps_the_gradients(calls):
+    ex, x = experts(), torch.ones(4, 16)
+    ex.forward(x, OFF)
+    calls.fail = ("moe_grouped_matmul_dx", 1)
+    with pytest.raises(L.MoeError):
+        ex.backward(x)
+    with pytest.raises(RuntimeError, match="forward"):
+        ex.backward(x)
+    ex.forward(x, OFF)
+    ex.backward(x)
+    assert flags(calls) == [OVER, OVER]  # nothing was there to add to
+
+
+@pytest.mark.parametrize("entry,nth", [("moe_swiglu_backward", 1), ("moe_grouped_matmul_dx", 2),
+                                       ("moe_grouped_matmul_dw", 2)])
+def test_backward_that_fails_between_the_gradients_asks_for_zero_grad(calls, entry, nth):
+    ex, x = experts(), torch.ones(4, 16)
+    ex.forward(x, OFF)
+    calls.fail = (entry, nth)
+    with pytest.raises(L.MoeError):
+        ex.backward(x)
+    ex.forward(x, OFF)
+    with pytest.raises(RuntimeError, match="zero_grad"):
+        ex.backward(x)
+    ex.zero_grad()
+    ex.backward(x)
+    assert flags(calls)[-2:] == [OVER, OVER]
+
+
+def test_gradients_add_up_until_zero_grad(calls):
+    ex, x = experts(), torch.ones(4, 16)
+    for zero in (False, False, True, False):
+        if zero:
+            ex.zero_grad()
+        ex.forward(x, OFF)
+        ex.backward(x)
+    assert flags(calls) == [OVER, OVER, ADD, ADD, OVER, OVER, ADD, ADD]

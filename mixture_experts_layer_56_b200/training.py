@@ -194,11 +194,11 @@ class LayerNorm:
         if dy.shape != x.shape or dy.dtype != x.dtype:
             raise ValueError("dy has to be like x")
         _same_stream(saved_on, stream)
-        self._saved = None
         with _on(stream):
             dx = torch.empty_like(x)
             # a workspace per call: captured ones may replay side by side
             ws = x.new_empty(max(256, L.moe_layer_norm_workspace_size(shape)), dtype=torch.uint8)
+        self._saved = None  # up to here an error changes nothing
         L.moe_layer_norm_backward(shape, dy, x, self.gamma, mean, rstd, dx, self.dgamma, self.dbeta,
                                   ws, stream=stream)
         return dx

@@ -110,3 +110,16 @@ def test_gradients_add_up_until_zero_grad(calls):
         ex.forward(x, OFF)
         ex.backward(x)
     assert flags(calls) == [OVER, OVER, ADD, ADD, OVER, OVER, ADD, ADD]
+
+
+def test_norm_backward_without_memory_changes_nothing(calls, monkeypatch):
+    nm, x = TR.LayerNorm(torch.ones(16)), torch.ones(4, 16)
+    nm.forward(x)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "empty_like", no_memory)
+        with pytest.raises(torch.OutOfMemoryError):
+            nm.backward(x)
+    nm.backward(x)
+    assert len(calls.named("moe_layer_norm_backward")) == 1
+    with pytest.raises(RuntimeError, match="forward"):
+        nm.backward(x)

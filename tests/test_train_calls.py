@@ -55,3 +55,46 @@ def test_orthogonalize_more_clusters_than_fit(r, c):
         ortho_call(m[i:i + 1].contiguous(), one)[0]()
         assert torch.equal(one[0], outs[0][i])
     assert [L.moe_read_status(ws) for _, ws in calls] == [0, 0]
+
+
+def test_inputs_let_go_of_while_a_side_stream_reads_them():
+    """Nothing but the module holds x, and nothing dy and u, once the calls have
+    returned: the current stream gets none of their memory before the side
+    stream, which starts late, is done."""
+    from mixture_experts_layer_56_b200 import training as TR
+    bf = torch.bfloat16
+    w13, w2 = randn(1, 4, 512, 192, dtype=bf) * 0.1, randn(2, 4, 192, 256, dtype=bf) * 0.1
+    gamma = randn(3, 192)
+    off = torch.tensor([0, 100, 100, 450, 600], dtype=torch.int32, device="cuda")
+
+    def run(stream=None):
+        ex, nm = TR.TrainableExperts(w13, w2), TR.LayerNorm(gamma)
+        x, u, dy, m = (randn(s, 600, 192, dtype=bf) for s in (4, 5, 6, 7))
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(200_000_000)  # some 100 ms
+        y = ex.forward(x, off.clone(), stream=stream)
+        h = nm.forward(u, stream=stream)
+        o = TR.orthogonalize(m.view(1, 600, 192), stream=stream)
+        del x, u, m
+        dx = ex.backward(dy, stream=stream)
+        du = nm.backward(dy, stream=stream)
+        del dy
+        return [y, h, o, dx, du, ex.dW13, ex.dW2, nm.dgamma], (ex, nm)
+
+    want, _ = run()
+    torch.cuda.synchronize()
+    junk = [torch.full((600, 192), 7.0, dtype=bf, device="cuda") for _ in range(16)]
+    torch.cuda.synchronize()
+    del junk
+    side = torch.cuda.Stream()
+    got, keep = run(side)
+    late = not side.query()
+    junk = [torch.full((600, 192), 7.0, dtype=bf, device="cuda") for _ in range(16)]
+    junk += [torch.zeros(5, dtype=torch.int32, device="cuda") for _ in range(16)]
+    assert late, "the side stream was done before the current one could get in its way"
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert keep[0].status() == 0 and junk

@@ -1,6 +1,8 @@
 """training.py's bookkeeping: what a call keeps, and leaves behind when it
 fails.  The library's entries are replaced by ones that record their calls; no
 GPU."""
+import contextlib
+
 import pytest
 import torch
 
@@ -39,6 +41,12 @@ def calls(monkeypatch):
         monkeypatch.setattr(L, name, lambda shape: 1 << 16)
     monkeypatch.setattr(L, "_stream", lambda stream: STREAM if stream is None else stream)
     monkeypatch.setattr(TR, "_on_current", lambda t, what: t)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: handle)
+    monkeypatch.setattr(TR, "_on", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, stream: seen.recorded.setdefault(stream, []).append(t),
+                        raising=False)
+    seen.recorded = {}
     return seen
 
 
@@ -123,3 +131,26 @@ def test_norm_backward_without_memory_changes_nothing(calls, monkeypatch):
     assert len(calls.named("moe_layer_norm_backward")) == 1
     with pytest.raises(RuntimeError, match="forward"):
         nm.backward(x)
+
+
+@pytest.mark.parametrize("stream", [None, STREAM, 77])
+def test_what_a_call_uses_is_recorded_on_a_stream_of_its_own(calls, stream):
+    """Everything passed to the library that was there before the call: the
+    caller's inputs and the module's own tensors."""
+    ex, nm = experts(), TR.LayerNorm(torch.ones(16), torch.ones(16))
+    u, dy, m, ws = torch.ones(4, 16), torch.ones(4, 16), torch.ones(2, 8, 16), torch.zeros(256)
+    x = nm.forward(u, stream=stream)
+    y = ex.forward(x, OFF, stream=stream)
+    dx = ex.backward(dy, stream=stream)
+    nm.backward(dx, stream=stream)
+    TR.orthogonalize(m, ws=ws, stream=stream)
+    assert y.shape == u.shape and all(s == stream for _, _, s in calls)
+    there = [u, dy, m, ws, OFF, x, dx, ex.W13, ex.W2, ex.ws, ex.dW13, ex.dW2, nm.gamma, nm.beta,
+             nm.dgamma, nm.dbeta]
+    used = {id(a) for _, args, _ in calls for a in args if isinstance(a, torch.Tensor)}
+    recorded = {id(t) for t in calls.recorded.get(stream, [])}
+    assert all(id(t) in used for t in there)
+    if stream == 77:
+        assert all(id(t) in recorded for t in there)
+    else:   # the current one
+        assert not calls.recorded

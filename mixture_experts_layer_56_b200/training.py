@@ -43,11 +43,17 @@ def _on_current(t, what):
     return t
 
 
+def _torch_stream(stream):
+    """The torch stream of a raw handle.  0 and 1 are the default stream's (for
+    0 ExternalStream makes a new one)."""
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream) if stream > 1 else torch.cuda.default_stream()
+
+
 def _on(stream):
     """A context in which torch allocates for ``stream``."""
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream))
 
 
 def _record(stream, *tensors):
@@ -55,8 +61,7 @@ def _record(stream, *tensors):
     by the time that they are let go of."""
     if stream is None or L._stream(stream) == L._stream(None):
         return  # 1 us a tensor, a step of 64 rows 112 us for 87
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
+    stream = _torch_stream(stream)
     for t in tensors:
         if t is not None:
             t.record_stream(stream)

@@ -98,3 +98,22 @@ def test_inputs_let_go_of_while_a_side_stream_reads_them():
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert keep[0].status() == 0 and junk
+
+
+def test_the_default_stream_by_its_raw_handle():
+    """stream=0 beside a current stream of its own: what the call allocates
+    belongs to the default stream."""
+    from mixture_experts_layer_56_b200 import training as TR
+    default, side = torch.cuda.default_stream(), torch.cuda.Stream()
+    for raw in (0, 1):
+        assert TR._torch_stream(raw) == default
+        with TR._on(raw):
+            assert torch.cuda.current_stream() == default
+    assert TR._torch_stream(side.cuda_stream).cuda_stream == side.cuda_stream
+    nm, x = TR.LayerNorm(torch.ones(64, device="cuda")), randn(1, 8, 64)
+    want = nm.forward(x)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        y = nm.forward(x, stream=0)
+        default.synchronize()
+        assert torch.equal(y, want)

@@ -154,3 +154,12 @@ def test_what_a_call_uses_is_recorded_on_a_stream_of_its_own(calls, stream):
         assert all(id(t) in recorded for t in there)
     else:   # the current one
         assert not calls.recorded
+
+
+def test_raw_handles_of_the_default_stream(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: "default")
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    assert [TR._on(h) for h in (0, 1, 4096)] == ["default", "default", ("external", 4096)]
+    with TR._on(None):
+        pass

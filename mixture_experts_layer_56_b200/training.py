@@ -100,6 +100,7 @@ class TrainableExperts:
         self.ws = _scratch(256, W13.device)
         self._saved = None
         self._have_grad = False
+        self._last = None  # raw stream of the last call
 
     def _shape(self, rows, n, k, flags=0):
         return L.make_grouped_shape(rows, self.n, n, k, _DTYPE[self.dtype], flags)
@@ -125,12 +126,13 @@ class TrainableExperts:
             gu, a = x.new_empty(rows, 2 * self.inter), x.new_empty(rows, self.inter)
             y = torch.empty_like(x)
         _record(stream, x, offsets, self.W13, self.W2, self.ws)
+        self._last = L._stream(stream)
         L.moe_grouped_matmul(self._shape(rows, 2 * self.inter, self.d), x, offsets, self.W13, gu,
                              self.ws, stream=stream)
         L.moe_swiglu(L.make_swiglu_shape(rows, self.inter, _DTYPE[self.dtype]), gu, a, stream=stream)
         L.moe_grouped_matmul(self._shape(rows, self.d, self.inter), a, offsets, self.W2, y, self.ws,
                              stream=stream)
-        self._saved = (x, offsets, gu, a, L._stream(stream))
+        self._saved = (x, offsets, gu, a, self._last)
         return y
 
     def backward(self, dy: torch.Tensor, stream=None) -> torch.Tensor:
@@ -171,8 +173,14 @@ class TrainableExperts:
         """The next ``backward`` overwrites dW13 and dW2."""
         self._have_grad = False
 
-    def status(self) -> int:
-        return L.moe_read_status(self.ws)
+    def status(self, stream=None) -> int:
+        """MOE_OK, or MOE_ERR_DEVICE_CHECK if a wait of a call before ran out;
+        clears it.  Waits for ``stream`` (None: that of the last forward or
+        backward, and the current one; replays of captured calls on another
+        stream need it named)."""
+        if stream is None and self._last not in (None, L._stream(None)):
+            _torch_stream(self._last).synchronize()
+        return L.moe_read_status(self.ws, stream=stream)
 
 
 class LayerNorm:

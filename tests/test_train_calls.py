@@ -117,3 +117,28 @@ def test_the_default_stream_by_its_raw_handle():
         y = nm.forward(x, stream=0)
         default.synchronize()
         assert torch.equal(y, want)
+
+
+def test_status_of_work_on_a_side_stream():
+    """A word that is written late, on the stream of the last call, is seen,
+    and cleared once."""
+    from mixture_experts_layer_56_b200 import training as TR
+    ex = TR.TrainableExperts(randn(1, 1, 128, 64), randn(2, 1, 64, 64))
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    x, side = randn(3, 8, 64), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ex.forward(x, off, stream=side)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # some 100 ms
+        ex.ws.view(torch.int32)[:1].fill_(L.MOE_ERR_DEVICE_CHECK)
+    assert not side.query()
+    assert ex.status() == L.MOE_ERR_DEVICE_CHECK
+    assert ex.status() == L.MOE_OK
+    ex.backward(x, stream=side)
+    assert ex.status(stream=side) == L.MOE_OK
+    # the last call on the default stream, the word asked for beside another one
+    ex.forward(x, off)
+    torch.cuda._sleep(200_000_000)
+    ex.ws.view(torch.int32)[:1].fill_(L.MOE_ERR_DEVICE_CHECK)
+    with torch.cuda.stream(side):
+        assert ex.status() == L.MOE_ERR_DEVICE_CHECK

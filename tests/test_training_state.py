@@ -163,3 +163,31 @@ def test_raw_handles_of_the_default_stream(monkeypatch):
     assert [TR._on(h) for h in (0, 1, 4096)] == ["default", "default", ("external", 4096)]
     with TR._on(None):
         pass
+
+
+def test_status_waits_for_the_stream_of_the_last_call(calls, monkeypatch):
+    """The word is read once the kernels that may write it are done."""
+    order = []
+
+    class Handle:
+        def __init__(self, raw):
+            self.raw = raw
+
+        def synchronize(self):
+            order.append(("wait", self.raw))
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Handle)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, stream: None, raising=False)
+    monkeypatch.setattr(L, "moe_read_status", lambda ws, stream=None: order.append(("read", stream)) or 0)
+    ex, x = experts(), torch.ones(4, 16)
+    ex.status()
+    ex.forward(x, OFF)
+    ex.status()
+    assert order == [("read", None)] * 2
+    order.clear()
+    ex.forward(x, OFF, stream=77)
+    ex.status()
+    ex.backward(x, stream=77)
+    ex.status()
+    ex.status(stream=78)
+    assert order == [("wait", 77), ("read", None)] * 2 + [("read", 78)]

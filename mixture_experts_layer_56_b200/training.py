@@ -238,18 +238,38 @@ class LayerNorm:
         return dx
 
 
+def _ortho_shape(m, steps):
+    if m.dim() != 3 or m.dtype not in _DTYPE or not m.is_contiguous():
+        raise ValueError("m has to be contiguous [n, rows, cols], bfloat16 or float32")
+    _on_current(m, "m")
+    return L.make_ortho_shape(*m.shape, steps, _DTYPE[m.dtype])
+
+
+def orthogonalize_workspace(m: torch.Tensor, steps: int = 5, stream=None) -> torch.Tensor:
+    """A workspace for ``orthogonalize`` of matrices like m, its status word
+    zeroed on ``stream``.  One can serve call after call on a stream, and
+    ``_lib.moe_read_status(ws, stream=stream)`` tells whether a wait of theirs
+    ran out."""
+    nbytes = max(256, L.moe_orthogonalize_workspace_size(_ortho_shape(m, steps)))
+    with _on(stream):
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=m.device)
+        ws[:4].zero_()
+    return ws
+
+
 def orthogonalize(m: torch.Tensor, steps: int = 5, coef=None, ws: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
     """Newton-Schulz orthogonalisation of each matrix of m [n, rows, cols], as
     bfloat16.  Of packed W13 matrices it is that of W1 on top of W3: the
-    packing permutes rows, which the iteration commutes with."""
-    if m.dim() != 3 or m.dtype not in _DTYPE or not m.is_contiguous():
-        raise ValueError("m has to be contiguous [n, rows, cols], bfloat16 or float32")
-    _on_current(m, "m")
-    shape = L.make_ortho_shape(*m.shape, steps, _DTYPE[m.dtype])
+    packing permutes rows, which the iteration commutes with.
+
+    Without ``ws`` the call takes its own, whose status nobody can read: pass
+    one of ``orthogonalize_workspace`` to learn of a wait that ran out."""
+    shape = _ortho_shape(m, steps)
     with _on(stream):
         if ws is None:
-            ws = _scratch(L.moe_orthogonalize_workspace_size(shape), m.device)
+            nbytes = max(256, L.moe_orthogonalize_workspace_size(shape))
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=m.device)
         o = torch.empty(m.shape, dtype=torch.bfloat16, device=m.device)
     _record(stream, m, ws)
     L.moe_orthogonalize(shape, m, o, ws, coef=coef, stream=stream)

@@ -142,3 +142,21 @@ def test_status_of_work_on_a_side_stream():
     ex.ws.view(torch.int32)[:1].fill_(L.MOE_ERR_DEVICE_CHECK)
     with torch.cuda.stream(side):
         assert ex.status() == L.MOE_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("shape", [(2, 64, 100), (2, 200, 300)])
+def test_orthogonalize_with_a_workspace_of_its_own(shape):
+    """One workspace serves call after call, and tells how they went."""
+    from mixture_experts_layer_56_b200 import training as TR
+    m = randn(1, *shape)
+    ws = TR.orthogonalize_workspace(m)
+    want = TR.orthogonalize(m)
+    for _ in range(2):
+        assert torch.equal(TR.orthogonalize(m, ws=ws), want)
+    assert L.moe_read_status(ws) == L.MOE_OK
+    # what it held does not matter
+    ws[4:] = 0xFF
+    assert torch.equal(TR.orthogonalize(m, ws=ws), want)
+    assert L.moe_read_status(ws) == L.MOE_OK
+    with pytest.raises(L.MoeError):
+        TR.orthogonalize(m, ws=ws[:128])

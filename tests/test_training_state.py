@@ -191,3 +191,20 @@ def test_status_waits_for_the_stream_of_the_last_call(calls, monkeypatch):
     ex.status()
     ex.status(stream=78)
     assert order == [("wait", 77), ("read", None)] * 2 + [("read", 78)]
+
+
+def test_a_workspace_is_not_zeroed_beyond_its_status_word(calls, monkeypatch):
+    """The workspace of a large stack is as large as its matrices."""
+    zeroed = []
+    real = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: zeroed.append(a) or real(*a, **kw))
+    monkeypatch.setattr(torch.Tensor, "zero_",
+                        lambda t: zeroed.append((t.numel() * t.element_size(),)) or t.fill_(0),
+                        raising=False)
+    m = torch.ones(2, 8, 16)
+    TR.orthogonalize(m)
+    assert zeroed == []
+    ws = TR.orthogonalize_workspace(m)
+    assert zeroed == [(4,)] and ws.numel() == 1 << 16 and (ws[:4] == 0).all()
+    TR.orthogonalize(m, ws=ws)
+    assert zeroed == [(4,)] and [a[3] is ws for a in calls.named("moe_orthogonalize")] == [False, True]

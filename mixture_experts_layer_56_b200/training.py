@@ -266,6 +266,9 @@ def orthogonalize(m: torch.Tensor, steps: int = 5, coef=None, ws: torch.Tensor |
     Without ``ws`` the call takes its own, whose status nobody can read: pass
     one of ``orthogonalize_workspace`` to learn of a wait that ran out."""
     shape = _ortho_shape(m, steps)
+    # the library writes ws_bytes from its first one on
+    if ws is not None and (ws.device != m.device or not ws.is_contiguous()):
+        raise ValueError("ws has to be contiguous, on the device of m")
     with _on(stream):
         if ws is None:
             nbytes = max(256, L.moe_orthogonalize_workspace_size(shape))

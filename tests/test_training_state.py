@@ -208,3 +208,13 @@ def test_a_workspace_is_not_zeroed_beyond_its_status_word(calls, monkeypatch):
     assert zeroed == [(4,)] and ws.numel() == 1 << 16 and (ws[:4] == 0).all()
     TR.orthogonalize(m, ws=ws)
     assert zeroed == [(4,)] and [a[3] is ws for a in calls.named("moe_orthogonalize")] == [False, True]
+
+
+def test_orthogonalize_refuses_a_workspace_that_is_not_memory_of_its_device(calls):
+    m = torch.ones(2, 8, 16)
+    for ws in (torch.empty(1 << 16, dtype=torch.uint8, device="meta"),
+               torch.empty(1 << 17, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="ws"):
+            TR.orthogonalize(m, ws=ws)
+    assert not calls
+    TR.orthogonalize(m, ws=torch.empty(1 << 14))

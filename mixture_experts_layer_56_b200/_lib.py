@@ -162,7 +162,7 @@ def strerror(code: int) -> str:
 
 
 def _ptr(x):
-    if x is None or type(x) is int:
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 

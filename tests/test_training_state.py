@@ -218,3 +218,11 @@ def test_orthogonalize_refuses_a_workspace_that_is_not_memory_of_its_device(call
             TR.orthogonalize(m, ws=ws)
     assert not calls
     TR.orthogonalize(m, ws=torch.empty(1 << 14))
+
+
+def test_pointers_of_subclasses_of_int():
+    class Address(int):
+        pass
+
+    assert L._ptr(Address(4096)) == 4096 and L._ptr(None) is None
+    assert L._ptr(torch.ones(1)) != 0

@@ -196,6 +196,7 @@ class LayerNorm:
         self.dgamma = torch.empty_like(gamma)
         self.dbeta = None if beta is None else torch.empty_like(beta)
         self._saved = None
+        self._have_grad = False
 
     def _shape(self, x):
         if x.dim() != 2 or x.shape[1] != self.gamma.shape[0] or x.dtype not in _DTYPE \
@@ -218,8 +219,10 @@ class LayerNorm:
         self._saved = (x, mean, rstd, L._stream(stream))
         return y
 
-    def backward(self, dy: torch.Tensor, stream=None) -> torch.Tensor:
-        """The gradient of ``forward``'s x; writes dgamma and dbeta."""
+    def backward(self, dy: torch.Tensor, stream=None, accumulate: bool = False) -> torch.Tensor:
+        """The gradient of ``forward``'s x; writes dgamma and dbeta, or adds to
+        what the ``backward`` calls since ``zero_grad`` left there (which
+        ``TrainableExperts.backward`` always does)."""
         if self._saved is None:
             raise RuntimeError("backward() without a forward() before it")
         x, mean, rstd, saved_on = self._saved
@@ -227,15 +230,30 @@ class LayerNorm:
         if dy.shape != x.shape or dy.dtype != x.dtype:
             raise ValueError("dy has to be like x")
         _same_stream(saved_on, stream)
+        dgamma, dbeta = self.dgamma, self.dbeta
+        add = accumulate and self._have_grad
         with _on(stream):
             dx = torch.empty_like(x)
             # a workspace per call: captured ones may replay side by side
             ws = x.new_empty(max(256, L.moe_layer_norm_workspace_size(shape)), dtype=torch.uint8)
+            if add:
+                dgamma = torch.empty_like(dgamma)
+                dbeta = None if dbeta is None else torch.empty_like(dbeta)
         self._saved = None  # up to here an error changes nothing
         _record(stream, dy, self.dgamma, self.dbeta)
-        L.moe_layer_norm_backward(shape, dy, x, self.gamma, mean, rstd, dx, self.dgamma, self.dbeta,
-                                  ws, stream=stream)
+        L.moe_layer_norm_backward(shape, dy, x, self.gamma, mean, rstd, dx, dgamma, dbeta, ws,
+                                  stream=stream)
+        if add:
+            with _on(stream):
+                self.dgamma += dgamma
+                if dbeta is not None:
+                    self.dbeta += dbeta
+        self._have_grad = True
         return dx
+
+    def zero_grad(self):
+        """The next ``backward`` overwrites dgamma and dbeta."""
+        self._have_grad = False
 
 
 def _ortho_shape(m, steps):

@@ -160,3 +160,31 @@ def test_orthogonalize_with_a_workspace_of_its_own(shape):
     assert L.moe_read_status(ws) == L.MOE_OK
     with pytest.raises(L.MoeError):
         TR.orthogonalize(m, ws=ws[:128])
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_norm_gradients_of_two_micro_batches(own_stream):
+    """Their sum is that of the two calls, rounded once, and not far from the
+    whole batch's."""
+    from mixture_experts_layer_56_b200 import training as TR
+    T, d = 300, 200
+    x, dy, gamma, beta = randn(1, 2 * T, d), randn(2, 2 * T, d), randn(3, d), randn(4, d)
+    stream = torch.cuda.Stream() if own_stream else None
+    torch.cuda.synchronize()
+    nm, parts = TR.LayerNorm(gamma, beta), []
+    for half in (slice(0, T), slice(T, 2 * T)):
+        alone = TR.LayerNorm(gamma, beta)
+        for n in (nm, alone):
+            n.forward(x[half], stream=stream)
+            n.backward(dy[half], stream=stream, accumulate=True)
+        parts.append(alone)
+    torch.cuda.synchronize()
+    for name in ("dgamma", "dbeta"):
+        a, b = (getattr(p, name) for p in parts)
+        assert torch.equal(getattr(nm, name), a + b)
+    X = x.double()
+    h = (X - X.mean(1, keepdim=True)) * (X.var(1, unbiased=False, keepdim=True) + 1e-5).rsqrt()
+    for got, ref, mag in ((nm.dgamma, (dy.double() * h).sum(0), (dy.double() * h).abs().sum(0)),
+                          (nm.dbeta, dy.double().sum(0), dy.double().abs().sum(0))):
+        # sums of 2 T terms, each from a dozen roundings of half a step
+        assert ((got.double() - ref).abs() <= (2 * T + 12) * 2.0 ** -24 * mag).all()

@@ -226,3 +226,36 @@ def test_pointers_of_subclasses_of_int():
 
     assert L._ptr(Address(4096)) == 4096 and L._ptr(None) is None
     assert L._ptr(torch.ones(1)) != 0
+
+
+@pytest.mark.parametrize("beta", [False, True])
+def test_norm_gradients_add_up_when_asked_to(calls, monkeypatch, beta):
+    """Two micro-batches: without accumulate the second one's gradients alone
+    remain, with it their sum; the first one after zero_grad writes."""
+    nm = TR.LayerNorm(torch.ones(16), torch.ones(16) if beta else None)
+    x, given = torch.ones(4, 16), []
+
+    def backward(shape, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
+        given.append((dgamma, dbeta))
+        for t in (dgamma, dbeta):
+            if t is not None:
+                t.fill_(float(dy[0, 0]))
+
+    monkeypatch.setattr(L, "moe_layer_norm_backward", backward)
+
+    def step(value, **kw):
+        nm.forward(x)
+        nm.backward(torch.full((4, 16), float(value)), **kw)
+        for t in (nm.dgamma, nm.dbeta):
+            if t is not None:
+                assert (t == t[0]).all()
+        assert (nm.dbeta is None) is not beta
+        return float(nm.dgamma[0] if not beta else nm.dbeta[0])
+
+    assert step(3, accumulate=True) == 3  # nothing was there
+    assert given[0][0] is nm.dgamma
+    assert step(4, accumulate=True) == 7
+    assert step(5) == 5
+    assert step(1, accumulate=True) == 6
+    nm.zero_grad()
+    assert step(2, accumulate=True) == 2

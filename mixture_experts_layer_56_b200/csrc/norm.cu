@@ -393,6 +393,9 @@ norm_fwd_kernel(const T* x, const float* __restrict__ gamma, const float* __rest
       const float e = of.x - mu;
       m2 = lanes_sum<W>(of.y + n_lane * (e * e));
     }
+    // Off by 2 steps at most.  1 / sqrtf, off by 1, stands in every row's way for
+    // 5 to 7% of the time (32768 x 4096 bf16 99 us for 93, 16384 x 4096 fp32 106
+    // for 99).
     const float rs = rsqrtf(m2 * inv_d + eps);
     if (!live) continue;
     m = pair(mu_w - mu, mu_w - mu);  // v is about the warp's mean already

@@ -188,3 +188,29 @@ def test_norm_gradients_of_two_micro_batches(own_stream):
                           (nm.dbeta, dy.double().sum(0), dy.double().abs().sum(0))):
         # sums of 2 T terms, each from a dozen roundings of half a step
         assert ((got.double() - ref).abs() <= (2 * T + 12) * 2.0 ** -24 * mag).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 512, 2048, 4096, 16384])
+def test_layer_norm_rstd_of_an_exact_variance(d, dtype):
+    """Rows of v and -v in turn, v of at most 11 bits: mean 0 and variance v^2
+    are exact, and rstd is off by rsqrtf's 2 steps at most, 4 x 2^-24.  (A
+    thread's sum of squares is k v^2 of 22 bits, exact for odd k up to 3, and
+    equal sums of all threads double exactly.)  Rows past the registers take 1 /
+    sqrtf: 2^-24 where the variance is exact, and so is its root.  With 32 values
+    per thread, at d = 16384 in float32, the sum goes through 20 v^2 and 28 v^2,
+    of 25 bits: two roundings of 5/8 and 7/8 of 2^-24 of the total, half of that
+    in its root, and the root's own: 2.75 x 2^-24."""
+    bits = 11 if dtype == torch.float32 else 8
+    v = (2 ** (bits - 1) + torch.arange(500, device="cuda") % 2 ** (bits - 1)).float()
+    v *= 2.0 ** (torch.arange(500, device="cuda") % 9 - 12)
+    x = v[:, None] * (1 - 2 * (torch.arange(d, device="cuda") % 2))
+    assert torch.equal(x, x.to(dtype).float())
+    x = x.to(dtype)
+    shape = L.make_norm_shape(500, d, DT[dtype], 0.0)
+    y, mean, rstd = torch.empty_like(x), torch.empty(500, device="cuda"), torch.empty(500, device="cuda")
+    L.moe_layer_norm(shape, x, torch.ones(d, device="cuda"), None, y, mean, rstd)
+    assert (mean == 0).all()
+    off = (rstd.double() * v.double() - 1).abs()
+    tol = 2.0 ** -24 * (4 if d < 16384 else 2.75 if dtype == torch.float32 else 1)
+    assert (off <= tol).all(), (int((off > tol).sum()), float(off.max()) * 2 ** 24)

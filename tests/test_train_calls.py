@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from mixture_experts_layer_56_b200 import _lib as L
+from tests.test_train_ops import U, assert_close, group_tol, ns64, ortho, ortho_check, run_grouped
 
 pytestmark = pytest.mark.gpu
 
@@ -214,3 +215,172 @@ def test_layer_norm_rstd_of_an_exact_variance(d, dtype):
     off = (rstd.double() * v.double() - 1).abs()
     tol = 2.0 ** -24 * (4 if d < 16384 else 2.75 if dtype == torch.float32 else 1)
     assert (off <= tol).all(), (int((off > tol).sum()), float(off.max()) * 2 ** 24)
+
+
+# ------------------------------------------------------ infinities and NaN
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_swiglu_of_infinities_and_nan(dtype):
+    """Each element is its own formula's: infinite and NaN where that is, the
+    bits of a run without them elsewhere."""
+    inf, nan = float("inf"), float("nan")
+    gu, da = randn(1, 9, 256, dtype=dtype), randn(2, 9, 128, dtype=dtype)
+    shape = L.make_swiglu_shape(9, 128, DT[dtype])
+
+    def run():
+        a, dgu = torch.empty_like(da), torch.empty_like(gu)
+        L.moe_swiglu(shape, gu, a)
+        L.moe_swiglu_backward(shape, gu, da, dgu)
+        return a.double(), dgu.double()
+
+    clean = run()
+    odd = torch.tensor([inf, -inf, nan], device="cuda", dtype=dtype)
+    gu[1, 3:6] = odd            # gates
+    gu[4, 64 + 9:64 + 12] = odd  # ups
+    da[7, 70:73] = odd
+    b = gu.double().view(9, -1, 2, 64)
+    g, u, d = b[:, :, 0], b[:, :, 1], da.double().view(9, -1, 64)
+    s = 1 / (1 + torch.exp(-g))
+    refs = ((g * s * u).reshape(9, -1),
+            torch.stack([d * u * s * (1 + g * (1 - s)), d * g * s], 2).reshape(9, -1))
+    for got, want, ref in zip(run(), clean, refs):
+        fine = ref.isfinite()
+        assert 3 <= int((~fine).sum()) <= 18
+        assert torch.equal(got[~fine].nan_to_num(7), ref[~fine].nan_to_num(7))
+        assert got[fine].isfinite().all()
+        # what has no odd operand keeps its bits
+        touched = torch.zeros(9, 2, 2, 64, dtype=torch.bool, device="cuda")
+        touched[1, 0, :, 3:6] = touched[4, 0, :, 9:12] = touched[7, 1, :, 6:9] = True
+        touched = (touched[:, :, 0] if got.shape[1] == 128 else touched).reshape(9, -1)
+        assert torch.equal(got[~touched], want[~touched])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [7, 72, 600, 1283, 4099, 4104, 8200, 20001])
+def test_layer_norm_of_infinities_and_nan(d, dtype):
+    """They stay in their row, and reach the columns' sums as any term does."""
+    T = 700
+    x, dy, gamma, beta = randn(1, T, d, dtype=dtype), randn(2, T, d, dtype=dtype), randn(3, d), randn(4, d)
+    shape = L.make_norm_shape(T, d, DT[dtype])
+    ws = torch.empty(L.moe_layer_norm_workspace_size(shape), dtype=torch.uint8, device="cuda")
+
+    def run():
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        st = [torch.empty(T, device="cuda") for _ in range(2)]
+        sums = [torch.empty(d, device="cuda") for _ in range(2)]
+        L.moe_layer_norm(shape, x, gamma, beta, y, *st)
+        L.moe_layer_norm_backward(shape, dy, x, gamma, *st, dx, *sums, ws)
+        return y.float(), dx.float(), *sums
+
+    y0, dx0, _, db0 = run()
+    x[3, d // 2], x[T - 1, 0], dy[350, d - 1] = float("nan"), float("inf"), float("nan")
+    y, dx, dg, db = run()
+    rows = torch.ones(T, dtype=torch.bool, device="cuda")
+    rows[[3, T - 1]] = False
+    assert torch.equal(y[rows], y0[rows]) and y[~rows].isnan().all()
+    rows[350] = False
+    assert torch.equal(dx[rows], dx0[rows]) and dx[~rows].isnan().all()
+    # every h of the two rows is NaN, and dy of one column
+    assert dg.isnan().all() and db[d - 1].isnan()
+    assert torch.equal(db[:d - 1], db0[:d - 1])
+
+
+# ------------------------------------------------- groups, sizes and types
+def heavy():
+    return [0] * 40 + [1400] + [1] * 22 + [78]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_grouped_where_one_group_has_nearly_all_rows(dtype):
+    """The averages that choose kernels and tiles say nothing of this group."""
+    run_grouped(heavy(), 136, 264, dtype, lead=1, tail=3, seed=3)
+    run_grouped([2] * 255 + [1000], 72, 40, dtype, seed=4)
+    run_grouped([0] * 200 + [3000] + [0] * 55, 264, 136, dtype, tail=1, seed=5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sizes,n,k", [([600, 0, 300, 5], 520, 776), ([3] * 40, 264, 1032),
+                                       ([0, 2000], 1288, 72), (heavy(), 136, 264)])
+def test_grouped_dw_in_f32_and_accumulated(sizes, n, k, dtype):
+    """Several tiles per group, written and then added to."""
+    G, rows = len(sizes), sum(sizes)
+    off = torch.tensor([0] + sizes).cumsum(0).int().cuda()
+    x, dy = randn(1, rows, k, dtype=dtype), randn(2, rows, n, dtype=dtype)
+    dw = torch.full((G, n, k), float("nan"), device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for flags in (L.MOE_GROUPED_DW_F32, L.MOE_GROUPED_DW_F32 | L.MOE_GROUPED_DW_ACCUMULATE):
+        before = dw.clone()
+        shape = L.make_grouped_shape(rows, G, n, k, DT[dtype], flags)
+        L.moe_grouped_matmul_dw(shape, dy, x, off, dw, ws)
+        for e in range(G):
+            a, b = int(off[e]), int(off[e + 1])
+            ref, tol = group_tol(dy[a:b].double().T, x[a:b].double(), b - a, dtype, torch.float32)
+            if flags & L.MOE_GROUPED_DW_ACCUMULATE:
+                # once per 8 rows where few rows are streamed, else once
+                times = (b - a + 7) // 8
+                mag = dy[a:b].double().abs().T @ x[a:b].double().abs() + before[e].double().abs()
+                ref, tol = ref + before[e].double(), tol + times * U * mag
+                if a == b:
+                    assert torch.equal(dw[e], before[e])
+            assert_close(dw[e], ref, tol, (flags, e))
+    assert L.moe_read_status(ws) == 0
+
+
+# ------------------------------------------------------------ Newton-Schulz
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,r,c", [(4, 33, 70), (4, 70, 33), (2, 128, 128), (1, 64, 2048),
+                                   (2, 2048, 128), (1, 128, 2049), (2, 129, 200), (1, 200, 129),
+                                   (2, 256, 264), (2, 300, 257), (2, 1000, 520), (1, 520, 1288)])
+def test_orthogonalize_keeps_its_documented_error(n, r, c, dtype):
+    """2e-3 of the norm, bf16's rounding (1.7e-3 of evenly spread values) among
+    it, with half as much again for single matrices: on chip, around the limits
+    of what stays there, and past them."""
+    m = randn(r + c, n, r, c, dtype=dtype)
+    ref = ns64(m)
+    off = (ortho(m).double() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)
+    assert (off <= 3e-3).all(), off
+
+
+def test_orthogonalize_sixteen_steps():
+    for r, c in ((40, 72), (72, 40), (160, 200)):
+        m = randn(r, 2, r, c)
+        ortho_check(m, steps=16, coef=[1.5, -0.5, 0.0] * 16)
+
+
+# ------------------------------------------------------------------- graphs
+def test_a_captured_step_of_the_module():
+    """training.py's calls in a graph, replayed on other inputs, beside an
+    eager step of the same weights."""
+    from mixture_experts_layer_56_b200 import training as TR
+    bf = torch.bfloat16
+    w13, w2, gamma = randn(1, 3, 256, 72, dtype=bf) * 0.1, randn(2, 3, 72, 128, dtype=bf) * 0.1, randn(3, 72)
+    off = torch.tensor([0, 50, 50, 90], dtype=torch.int32, device="cuda")
+    u, dy = randn(4, 90, 72, dtype=bf), randn(5, 90, 72, dtype=bf)
+
+    def make():
+        ex, nm = TR.TrainableExperts(w13, w2), TR.LayerNorm(gamma)
+
+        def step():
+            y = ex.forward(nm.forward(u), off)
+            du = nm.backward(ex.backward(dy), accumulate=True)
+            return y, du, TR.orthogonalize(ex.dW2)
+        return ex, nm, step
+
+    ex, nm, step = make()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (6, 7):
+        u.copy_(randn(seed, 90, 72, dtype=bf))
+        # the captured backward adds to what is there: the same start for both
+        eager = make()
+        eager[2]()
+        for mine, theirs in ((ex.dW13, eager[0].dW13), (ex.dW2, eager[0].dW2), (nm.dgamma, eager[1].dgamma)):
+            mine.copy_(theirs)
+        want = eager[2]()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip([*got, ex.dW13, ex.dW2, nm.dgamma],
+                        [*want, eager[0].dW13, eager[0].dW2, eager[1].dgamma]):
+            assert torch.equal(a, b)

@@ -37,9 +37,12 @@ constexpr int kSmMaxSlices = 4;
 constexpr int kSmMaxCtas = 8;
 constexpr int kSmSquare = 2 * kSmSlice;    // A or B: 128 x 128 fp16, two k-blocks
 constexpr int kSmPart = kSmSide * kSmSide * 4;
-// at least this much, so that an SM holds one CTA: with two, clusters could
-// wait for one another's tensor memory
-constexpr int kSmLeast = 120 * 1024;
+// At least this much, so that an SM holds no other kernel's tensor memory beside
+// a CTA's, which takes all of it: two clusters, each with a CTA that has its
+// columns and one that waits for the other's, would wait for good.  The 67 KB
+// left over are less than four stages of a 128-row pair's pipeline.  (With 200
+// KB, L1 is short of M's second reading: five of 128 x 512 46.7 us for 44.8.)
+constexpr int kSmLeast = 160 * 1024;
 
 struct OrthoCoef {
   float v[3 * 16];

@@ -383,11 +383,14 @@ int moe_layer_norm_backward(const moe_norm_shape_t* shape, const void* dy, const
    `coef` is HOST memory, (a, b, c) for each step, read before the call
    returns; NULL means 3.4445, -4.7750, 2.0315 in each.  O [n_mats, rows,
    cols] is bfloat16, whatever the dtype of M.  The products run on the tensor
-   cores with fp16 operands beside a 22-bit X, which needs the coefficients to
-   keep the singular values of every step's X below about 10 (the defaults keep
-   them below 1.25), and O's error relative to its norm is about 2e-3, bf16's
-   own rounding among it (which for a matrix of one entry can be 2^-8 by itself).  Entries of X below about 2^-24 / sqrt(max(rows,
-   cols)) are lost, as in matrices whose norm is far below the 1e-7.  A matrix of
+   cores with fp16 operands beside a 22-bit X, whatever the dtype of M, which
+   needs the coefficients to keep the singular values of every step's X below
+   about 10 (the defaults keep them below 1.25).  O's error relative to its norm
+   is about 2e-3 for random matrices and up to 2.6e-3 where all singular values
+   are alike, bf16's own rounding of 1.7e-3 among it (which for a matrix of one
+   value can be 2^-8 by itself).  Entries of X below about 2^-24 /
+   sqrt(max(rows, cols)) are lost, as in matrices whose norm is far below the
+   1e-7.  A matrix of
    zeros gives zeros; one with an infinity or NaN gives NaN, the others of the
    stack are untouched by it.  M's tensor may have any 1 <= rows, cols <=
    65536; n_mats <= 65535; 1 <= steps <= 16. */

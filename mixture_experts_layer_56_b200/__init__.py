@@ -10,7 +10,8 @@ Python side:
   ``moe_layer_forward_host`` on pinned host buffers.
 * ``training``: ``TrainableExperts`` (gate/up product, SwiGLU, down product and
   their gradients over the rows of a dispatch), ``LayerNorm`` and
-  ``orthogonalize`` (the Muon optimiser's update of the stacked matrices).
+  ``orthogonalize`` (the Muon optimiser's update of the stacked matrices;
+  ``orthogonalize_workspace`` for a call whose status is read).
 * ``synthetic``: seeded counter-based inputs of the benchmark workloads (no
   layer arithmetic).
 

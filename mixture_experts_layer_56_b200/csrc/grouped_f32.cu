@@ -12,7 +12,8 @@
 //
 // The weight gradient, whose reduction is a group's rows, sums 128 products at
 // a time and adds these sums up apart, which keeps the rounding of long groups
-// near sqrt(128) rather than sqrt(rows) half steps.  The other two sum a
+// near sqrt(128) rather than sqrt(rows) half steps (its kernel for few rows adds 8
+// at a time to what lies in memory).  The other two sum a
 // matrix's width in one chain, as two blocks per SM leave no registers for
 // more (8 x 1024 x 2048 x 1024: 54 TFLOP/s; with apart sums 6% less).
 #include <cuda_runtime.h>
@@ -288,10 +289,12 @@ grouped_f32_kernel(const float* __restrict__ a, const float* __restrict__ b,
   }
 }
 
-// Few rows per group: the matrices are streamed once, up to kFewR rows of the
-// group with them, and bound by memory (40 groups of one row of 2392 x 1528:
+// Few rows per group: a matrix is streamed once for every kFewR rows of its
+// group, and one pass is bound by memory (40 groups of one row of 2392 x 1528:
 // forward 109 us, 5.4 TB/s, input gradient 121; in 64 x 64 tiles, almost all of
-// each of them empty, 594 and 694).
+// each of them empty, 594 and 694).  More passes than one are not: 16 groups of 16
+// rows of 2048 x 1024 68 and 59 us, of 30 rows 146 (in tiles) and 102, where the
+// bytes take 21.
 constexpr int kFewR = 8;
 constexpr int kFewK = 1024;  // reduction steps of the rows in shared memory at a time
 
@@ -616,7 +619,10 @@ int launch_grouped_f32(int dir, const float* a, const float* b, const int32_t* o
                        cudaStream_t st) {
   const int64_t N = dir == kGroupedFwd ? n : k;
   const int64_t some = rows < groups ? rows : groups;  // groups with rows, at most
-  // Few rows per group, on average (16 groups of 2048 x 1024 forward, 24 rows: 95
+  // Few rows per group, on average, which is all that the host knows.  A group far
+  // above it is the same work in passes of 8 rows: 64 groups of 1024 x 1024, all
+  // of 1500 rows in one, forward 131 us (142 for that group alone), input gradient
+  // 106 (150), weight gradient 191 (104).  (16 groups of 2048 x 1024 forward, 24 rows: 95
   // us for 145 in tiles, 40 rows: 154 for 147; input gradient, 24: 88 for 143, 40:
   // 145 for 145).
   if (dir != kGroupedDw && rows <= (dir == kGroupedFwd ? 24ll : 32ll) * groups) {

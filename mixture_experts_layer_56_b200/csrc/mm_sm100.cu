@@ -27,12 +27,16 @@
 // last one in both operands in shared memory before the MMAs may read it.
 //
 // Bound by the tensor cores (full groups), whose rate under long loads is the
-// power cap's: 16 groups of 4096 rows of 2048 x 2048 forward 375 us, 1466
-// TFLOP/s (the library's best single product of 8192 cubed reaches 1643, and
-// 1369 in a loop); 63 groups of some 910 rows of 1792 x 1280 250 us, 1050
+// power cap's: 16 groups of 4096 rows of 2048 x 2048 forward 444 us in a loop,
+// 1240 TFLOP/s, and 375 rested (the library's best single product of 8192 cubed:
+// 1369 and 1643 TFLOP/s); 63 groups of some 910 rows of 1792 x 1280 270 us, 975
 // TFLOP/s, a last tile per group being part empty; the weight gradient at 1784 x
 // 1288 362 us, whose row pitches are no multiple of 128 bytes and cost the TMA
-// loads and L2 a third.  Bound by memory (few rows per group): 8 tokens x 6 of 64
+// loads and L2 a third.  A float32 weight gradient costs its stores (64 groups of
+// 12 rows of 2816 x 2048: 253 us, 148 in bf16, of 227 and 113 for the bytes); one
+// that is added to reads the old values a piece at a time behind the accumulator
+// and takes 1744 there, 1801 for 1044 with 1536 rows per group.  Its reduction is
+// not split: one group of 16384 rows of 256 x 256 is four tiles, 72 us.  Bound by memory (few rows per group): 8 tokens x 6 of 64
 // experts of 2816 x 2048 63 us, 0.98 of the rate of a copy.
 #include <cuda.h>
 #include <cuda_fp16.h>

@@ -5,8 +5,8 @@
 //   dx = s (v - mean v - h mean(v h)), v = dy gamma
 //   dgamma = sum_t dy h,  dbeta = sum_t dy
 //
-// Bound by memory: 32768 x 4096 bf16 forward 88 us (6.1 TB/s, 0.93 of the
-// measured copy rate), backward 143 us (5.6 TB/s, 0.86).
+// Bound by memory: 32768 x 4096 bf16 forward 88 to 97 us (5.5 to 6.1 TB/s, 0.85 to
+// 0.93 of the measured copy rate), backward 143 to 148 us (5.5 TB/s, 0.84).
 //
 // A row is read once and held in registers: a group of 32 to 512 threads per
 // row, kVals values each, so that the variance is taken about the mean (a second
@@ -422,7 +422,8 @@ __device__ __forceinline__ void load_n(const T* p, float* v) {
 }
 
 // Rows that the registers do not hold: three reads of x, the last two from L1
-// and L2 (8192 x 16384 bf16 forward 129 us, 4.2 TB/s; backward 265 us).  N values
+// and L2 (8192 x 16384 bf16 forward 131 us, 4.1 TB/s, backward 271; 4096 x 5120 and
+// 8192 fp32 42 and 47 us, backward 93 and 127, 1.1 to 2.4 times the bytes').  N values
 // per access: a 16-byte piece, or one where rows are not whole pieces.
 template <typename T, int N>
 __global__ void __launch_bounds__(512)

@@ -22,9 +22,10 @@
 // the diagonal are computed, and written twice.
 //
 // Bound by the tensor cores and the power cap: 64 matrices of 2048 x 1408, five
-// steps, 4.79 TFLOP (symmetric halves counted once), 5.4 ms while the clock is at
-// 1.9 GHz, 6.4 when the cap holds it near 1.2 GHz; per step A takes 235 us, B 197
-// and the update 510 (it reads hi, lo and writes both beside its product, 1.5 GB).
+// steps, 4.79 TFLOP (symmetric halves counted once), 6.4 ms call after call, the
+// cap holding the clock near 1.2 GHz, and 5.4 rested at 1.9 GHz; per step, rested,
+// A takes 235 us, B 197 and the update 510 (it reads hi, lo and writes both beside
+// its product, 1.5 GB).
 // Matrices of few hundred rows are bound by three launches a step of about 10 us
 // each: one of 256 x 256 108 us, five of 640 x 560 167.
 #include <cuda.h>

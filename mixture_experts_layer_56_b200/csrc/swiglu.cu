@@ -8,8 +8,8 @@
 //
 // Bound by memory: 3 (5) values per output element, each moved once in
 // 16-byte pieces; arithmetic in fp32, one rounding on the store.  bf16, 57344 x
-// 896: 50 us, 6.2 TB/s (0.95 of a copy's rate); backward, 98304 x 1408: 199 us,
-// 6.9 TB/s (what L2 still holds of the last call's output need not be written).
+// 896: 50 us, 6.1 TB/s (0.94 of a copy's rate); backward, 98304 x 1408: 197 us,
+// 7.0 TB/s (what L2 still holds of the last call's output need not be written).
 // A thread does one piece of each operand, so that a grid of many blocks keeps
 // enough loads in flight; a loop over a resident grid was no faster.
 #include <cuda_runtime.h>
@@ -22,7 +22,8 @@ namespace moe {
 namespace {
 
 // bf16 results: ex2.approx and rcp.approx, a few fp32 ulp, far below the
-// store's rounding.  e^-g that overflows gives s = 0.
+// store's rounding.  Below g = -87.3, where s would be subnormal, and where e^-g
+// overflows it is 0, off by 2^-126 at most.
 __device__ __forceinline__ float sigmoid_of(float g, bf16) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));

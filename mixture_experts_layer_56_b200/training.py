@@ -83,7 +83,9 @@ class TrainableExperts:
 
     ``W13`` [n, 2*inter, d] is packed as by ``moe_pack_w13``, ``W2`` is
     [n, d, inter].  ``dW13`` and ``dW2`` are float32, accumulated over the
-    ``backward`` calls since ``zero_grad``."""
+    ``backward`` calls since ``zero_grad``.  Rows that no expert owns (behind the
+    last offset of a padded batch) reach none of them; in the results they hold
+    anything."""
 
     def __init__(self, W13: torch.Tensor, W2: torch.Tensor):
         n, two_inter, d = W13.shape

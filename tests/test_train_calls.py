@@ -384,3 +384,21 @@ def test_a_captured_step_of_the_module():
         for a, b in zip([*got, ex.dW13, ex.dW2, nm.dgamma],
                         [*want, eager[0].dW13, eager[0].dW2, eager[1].dgamma]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("one_sign,per_row", [(False, 1.5e-9), (True, 6e-9)])
+def test_dw_in_f32_keeps_its_documented_error(one_sign, per_row):
+    """The header's figures for long groups, with half a step of float32 on top
+    (and, for mixed signs, half as much again for one matrix of 64 x 72)."""
+    for rows in (1000, 16384, 60000):
+        x, dy = randn(1, rows, 72, dtype=torch.bfloat16), randn(2, rows, 64, dtype=torch.bfloat16)
+        if one_sign:
+            x, dy = x.abs(), dy.abs()
+        off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        dw = torch.empty(1, 64, 72, device="cuda")
+        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        L.moe_grouped_matmul_dw(L.make_grouped_shape(rows, 1, 64, 72, L.MOE_DTYPE_BF16, L.MOE_GROUPED_DW_F32),
+                                dy, x, off, dw, ws)
+        ref = dy.double().T @ x.double()
+        off_ = float((dw[0].double() - ref).norm() / ref.norm())
+        assert off_ <= per_row * rows + U, (rows, off_ / rows)
